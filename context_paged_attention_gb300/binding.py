@@ -9,6 +9,7 @@ documented dtype; the current torch stream is used unless one is given.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -18,10 +19,13 @@ from .build_lib import LIB
 DTYPE_BF16 = 0
 DTYPE_FP32 = 1
 DTYPE_FP8_E4M3 = 2  # pools only
+DTYPE_FP4_E2M1 = 3  # pools only: 4-bit codes with an E4M3 scale per 16 values
 FP8_NAN_CODE = 0x7F
 LSE_TOKEN_MAJOR = 0
 LSE_HEAD_MAJOR = 1
 MAX_MERGE_VIEWS = 16
+ROPE_HALVES = 0  # pairs (i, i + rot_dim / 2)
+ROPE_PAIRS = 1  # pairs (2 i, 2 i + 1)
 
 _STATUS_NAMES = {
     0: "CPATTN_OK",
@@ -62,8 +66,18 @@ class PoolDesc(ctypes.Structure):
         return self.head_dim_v != self.head_dim
 
     def pool_shape(self, value: bool = False):
+        """Shape of a pool tensor; a 4-bit pool is one flat byte buffer (``fp4_views`` splits it)."""
         d = self.head_dim_v if value else self.head_dim
-        return (self.P, self.num_pages, self.num_kv_heads, self.page_size // self.P, d)
+        shape = (self.P, self.num_pages, self.num_kv_heads, self.page_size // self.P, d)
+        return (math.prod(shape[:-1]) * (d // 2 + d // 16),) if self.fp4 else shape
+
+    def fp4_views(self, pool, value: bool = False):
+        """Views of a 4-bit pool's codes ``[P, pages, heads, slots, D / 2]`` and
+        scales ``[..., D / 16]`` (E4M3 codes), both uint8."""
+        d = self.head_dim_v if value else self.head_dim
+        rows = (self.P, self.num_pages, self.num_kv_heads, self.page_size // self.P)
+        n = math.prod(rows) * d // 2
+        return pool[:n].view(*rows, d // 2), pool[n:].view(*rows, d // 16)
 
     def torch_dtype(self):
         """Type of queries, new K/V and outputs."""
@@ -73,9 +87,13 @@ class PoolDesc(ctypes.Structure):
     def fp8(self) -> bool:
         return self.kv_dtype == DTYPE_FP8_E4M3
 
+    @property
+    def fp4(self) -> bool:
+        return self.kv_dtype == DTYPE_FP4_E2M1
+
     def pool_torch_dtype(self):
-        """Element type of pool_k / pool_v tensors (E4M3 codes as uint8)."""
-        return torch.uint8 if self.fp8 else self.torch_dtype()
+        """Element type of pool_k / pool_v tensors (E4M3 and E2M1 codes as uint8)."""
+        return torch.uint8 if self.fp8 or self.fp4 else self.torch_dtype()
 
 
 class PartialView(ctypes.Structure):
@@ -91,6 +109,12 @@ class PartialView(ctypes.Structure):
     ]
 
 
+class ScoreMod(ctypes.Structure):
+    """Mirror of ``cpattn_score_mod``; made by ``score_mod``, which keeps the tensors alive."""
+
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -98,6 +122,7 @@ _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
 _pdesc = ctypes.POINTER(PoolDesc)
+_pmod = ctypes.POINTER(ScoreMod)
 
 _SIGNATURES = {
     "cpattn_version": (_i32, []),
@@ -116,6 +141,14 @@ _SIGNATURES = {
     "cp_paged_attn_fused_workspace_bytes": (_sz, [_pdesc, _i32, _i32, _i32]),
     "own_token_attn": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _f32,
                               _vp, _vp, _vp]),
+    "cp_rope_kv_write": (_i32, [_pdesc, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32,
+                                _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "cp_paged_attn_partial_mod": (_i32, [_pdesc, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _f32,
+                                         _vp, _vp, _i32, _vp, _pmod, _vp, _sz, _vp, _vp]),
+    "cp_paged_attn_fused_mod": (_i32, [_pdesc, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _f32,
+                                       _vp, _vp, _i32, _vp, _vp, _pmod, _vp, _sz, _vp, _vp]),
+    "own_token_attn_mod": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _f32,
+                                  _pmod, _vp, _vp, _vp]),
     "lse_merge": (_i32, [_i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
 }
 
@@ -189,6 +222,62 @@ def cp_kv_write(desc: PoolDesc, pool_k, pool_v, k_new, v_new, positions, qo_indp
     _check(st, "cp_kv_write")
 
 
+def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions, qo_indptr, kv_page_indptr,
+                     kv_page_indices, cos_sin, q_out, k_out=None, rot_begin=0, style=ROPE_HALVES, dev_status=None,
+                     stream=None):
+    """Rotate queries and new keys and write K/V into the pool (see ``cp_rope_kv_write`` in cpattn.h).
+
+    ``cos_sin [positions, rot_dim]`` fp32: ``rot_dim / 2`` cosines, then the sines, a row a position.
+    ``q`` and ``q_out`` may both be None (keys only); ``q_out`` may be ``q`` and ``k_out`` ``k_new``."""
+    lib = load_library()
+    T = positions.numel()
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
+    for name, x, heads, d in (("q", q, None, desc.head_dim), ("q_out", q_out, None, desc.head_dim),
+                              ("k_new", k_new, desc.num_kv_heads, desc.head_dim),
+                              ("k_out", k_out, desc.num_kv_heads, desc.head_dim),
+                              ("v_new", v_new, desc.num_kv_heads, desc.head_dim_v)):
+        if x is None:
+            continue
+        if x.dtype != desc.torch_dtype():
+            raise TypeError(f"{name} must have the layer's dtype {desc.torch_dtype()}")
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != d or (heads is not None and x.shape[1] != heads):
+            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {d}]")
+    if q is not None and q_out is not None and q.shape != q_out.shape:
+        raise ValueError("q_out must have q's shape")
+    st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
+                              0 if q is None else q.shape[1], _i32_tensor(positions, "positions"),
+                              _i32_tensor(qo_indptr, "qo_indptr"), qo_indptr.numel() - 1, T,
+                              _i32_tensor(kv_page_indptr, "kv_page_indptr"),
+                              _i32_tensor(kv_page_indices, "kv_page_indices"), _ptr(cos_sin), cos_sin.shape[0],
+                              int(rot_begin), cos_sin.shape[1], int(style), _ptr(q_out), _ptr(k_out),
+                              _i32_tensor(dev_status, "dev_status"), _stream(stream))
+    _check(st, "cp_rope_kv_write")
+
+
+def score_mod(softcap=0.0, slopes=None, positions=None):
+    """A ``ScoreMod`` for the ``mod`` argument of the attention calls (see
+    ``cpattn_score_mod`` in cpattn.h): scores capped by ``softcap * tanh(s /
+    softcap)``, then ``slopes[head] * (key position - query position)`` added."""
+    if slopes is not None and slopes.dtype != torch.float32:
+        raise TypeError("slopes must be float32")
+    m = ScoreMod(float(softcap), _ptr(slopes), _i32_tensor(positions, "positions"))
+    m.tensors = (slopes, positions)
+    return m
+
+
+def _mod(mod, heads, tokens):
+    """Pointer to a ScoreMod for a call of that many query heads and tokens, or None."""
+    if mod is None:
+        return None
+    slopes, positions = mod.tensors
+    if slopes is not None and slopes.numel() != heads:
+        raise ValueError(f"slopes must have one value for each of the {heads} query heads")
+    if positions is not None and positions.numel() != tokens:
+        raise ValueError(f"positions must have one value for each of the {tokens} tokens")
+    return ctypes.byref(mod)
+
+
 def workspace_bytes(desc: PoolDesc, num_q_heads: int, num_tokens: int, max_kv_len: int) -> int:
     return load_library().cp_paged_attn_workspace_bytes(ctypes.byref(desc), num_q_heads, num_tokens, max_kv_len)
 
@@ -216,38 +305,40 @@ def fused_workspace_bytes(desc: PoolDesc, num_q_heads: int, num_tokens: int, max
 
 def cp_paged_attn_fused(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_len, kv_page_indptr, kv_page_indices,
                         scale, out, workspace, lse_out=None, extra_o=None, extra_lse=None, qo_indptr=None,
-                        num_rows=None, row_order=None, dev_status=None, stream=None):
-    """All partners' partials and their merge in one launch (see ``cp_paged_attn_fused`` in cpattn.h)."""
+                        num_rows=None, row_order=None, dev_status=None, stream=None, mod=None):
+    """All partners' partials and their merge in one launch (see ``cp_paged_attn_fused`` in cpattn.h);
+    ``mod``: modified scores (``score_mod``)."""
     lib = load_library()
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
     dt = DTYPE_BF16 if out.dtype == torch.bfloat16 else DTYPE_FP32
-    st = lib.cp_paged_attn_fused(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
-                                 _i32_tensor(qo_indptr, "qo_indptr"), _i32_tensor(kv_len, "kv_len"),
-                                 int(max_kv_len), _i32_tensor(kv_page_indptr, "kv_page_indptr"),
-                                 _i32_tensor(kv_page_indices, "kv_page_indices"),
-                                 _i32_tensor(row_order, "row_order"), float(scale), _ptr(extra_o),
-                                 _ptr(extra_lse), dt, _ptr(out), _ptr(lse_out), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(),
-                                 _i32_tensor(dev_status, "dev_status"), _stream(stream))
+    st = lib.cp_paged_attn_fused_mod(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
+                                     _i32_tensor(qo_indptr, "qo_indptr"), _i32_tensor(kv_len, "kv_len"),
+                                     int(max_kv_len), _i32_tensor(kv_page_indptr, "kv_page_indptr"),
+                                     _i32_tensor(kv_page_indices, "kv_page_indices"),
+                                     _i32_tensor(row_order, "row_order"), float(scale), _ptr(extra_o),
+                                     _ptr(extra_lse), dt, _ptr(out), _ptr(lse_out), _mod(mod, Hq, T), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(),
+                                     _i32_tensor(dev_status, "dev_status"), _stream(stream))
     _check(st, "cp_paged_attn_fused")
 
 
 def cp_paged_attn_partial_ex(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_len, kv_page_indptr,
                              kv_page_indices, scale, o_part, lse_part, workspace, lse_layout=LSE_TOKEN_MAJOR,
-                             qo_indptr=None, num_rows=None, row_order=None, dev_status=None, stream=None):
-    """cp_paged_attn_partial with the LSE layout chosen (see ``cp_paged_attn_partial_ex`` in cpattn.h)."""
+                             qo_indptr=None, num_rows=None, row_order=None, dev_status=None, stream=None, mod=None):
+    """cp_paged_attn_partial with the LSE layout chosen (see ``cp_paged_attn_partial_ex`` in cpattn.h);
+    ``mod``: modified scores (``score_mod``)."""
     lib = load_library()
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
-    st = lib.cp_paged_attn_partial_ex(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
-                                      _i32_tensor(qo_indptr, "qo_indptr"), _i32_tensor(kv_len, "kv_len"),
-                                      int(max_kv_len), _i32_tensor(kv_page_indptr, "kv_page_indptr"),
-                                      _i32_tensor(kv_page_indices, "kv_page_indices"), float(scale), _ptr(o_part),
-                                      _ptr(lse_part), int(lse_layout), _i32_tensor(row_order, "row_order"),
-                                      _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(),
-                                      _i32_tensor(dev_status, "dev_status"), _stream(stream))
+    st = lib.cp_paged_attn_partial_mod(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
+                                       _i32_tensor(qo_indptr, "qo_indptr"), _i32_tensor(kv_len, "kv_len"),
+                                       int(max_kv_len), _i32_tensor(kv_page_indptr, "kv_page_indptr"),
+                                       _i32_tensor(kv_page_indices, "kv_page_indices"), float(scale), _ptr(o_part),
+                                       _ptr(lse_part), int(lse_layout), _i32_tensor(row_order, "row_order"),
+                                       _mod(mod, Hq, T), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(),
+                                       _i32_tensor(dev_status, "dev_status"), _stream(stream))
     _check(st, "cp_paged_attn_partial_ex")
 
 
@@ -273,17 +364,20 @@ def lse_merge_views(views, num_tokens, num_heads, head_dim_v, out, out_stride_to
     _check(st, "lse_merge_views")
 
 
-def own_token_attn(q, k_new, v_new, qo_indptr, num_real_rows, max_q_len, scale, o_own, lse_own, stream=None):
+def own_token_attn(q, k_new, v_new, qo_indptr, num_real_rows, max_q_len, scale, o_own, lse_own, stream=None,
+                   mod=None):
     """Causal attention of the step's new tokens (see ``own_token_attn`` in cpattn.h);
-    with ``v_new`` None the value width is ``o_own``'s (MLA: the first 512 key values)."""
+    with ``v_new`` None the value width is ``o_own``'s (MLA: the first 512 key values);
+    ``mod``: modified scores (``score_mod``; its positions are not used)."""
     lib = load_library()
     T, Hq, D = q.shape
     Hkv = k_new.shape[1]
     Dv = o_own.shape[-1] if v_new is None else v_new.shape[2]
     dt = DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_FP32
-    st = lib.own_token_attn(_ptr(q), _ptr(k_new), _ptr(v_new), Hq, Hkv, D, Dv, dt,
-                            _i32_tensor(qo_indptr, "qo_indptr"), qo_indptr.numel() - 1, int(num_real_rows), T,
-                            int(max_q_len), float(scale), _ptr(o_own), _ptr(lse_own), _stream(stream))
+    st = lib.own_token_attn_mod(_ptr(q), _ptr(k_new), _ptr(v_new), Hq, Hkv, D, Dv, dt,
+                                _i32_tensor(qo_indptr, "qo_indptr"), qo_indptr.numel() - 1, int(num_real_rows), T,
+                                int(max_q_len), float(scale), _mod(mod, Hq, T), _ptr(o_own), _ptr(lse_own),
+                                _stream(stream))
     _check(st, "own_token_attn")
 
 

@@ -24,12 +24,18 @@ int interleave_of(const cpattn_pool_desc* d) { return d->interleave > 1 ? d->int
 // Pool element type: kv_dtype 0 means the layer's dtype.
 int kv_dtype_of(const cpattn_pool_desc* d) { return d->kv_dtype == 0 ? d->dtype : d->kv_dtype; }
 
-int kv_bytes(const cpattn_pool_desc* d) {
-  const int kt = kv_dtype_of(d);
-  return kt == CPATTN_DTYPE_FP8_E4M3 ? 1 : dtype_bytes(kt);
+bool is_fp8(const cpattn_pool_desc* d) { return kv_dtype_of(d) == CPATTN_DTYPE_FP8_E4M3; }
+bool is_fp4(const cpattn_pool_desc* d) { return kv_dtype_of(d) == CPATTN_DTYPE_FP4_E2M1; }
+
+// Bytes of a pool row of n values (E2M1: its codes, without the block scales).
+int row_bytes(const cpattn_pool_desc* d, int n) {
+  return is_fp4(d) ? n / 2 : (is_fp8(d) ? n : n * dtype_bytes(kv_dtype_of(d)));
 }
 
-bool is_fp8(const cpattn_pool_desc* d) { return kv_dtype_of(d) == CPATTN_DTYPE_FP8_E4M3; }
+// Rows of a pool tensor: [P][num_pages][num_kv_heads][page_size / P].
+int64_t pool_rows(const cpattn_pool_desc* d) {
+  return static_cast<int64_t>(d->num_pages) * d->num_kv_heads * d->page_size;
+}
 
 // Common descriptor checks.
 int check_desc(const cpattn_pool_desc* d) {
@@ -41,15 +47,17 @@ int check_desc(const cpattn_pool_desc* d) {
   const int eb = dtype_bytes(d->dtype);
   if (eb == 0) return CPATTN_ERR_INVALID_ARG;
   const int kt = kv_dtype_of(d);
-  if (kt != d->dtype && kt != CPATTN_DTYPE_FP8_E4M3) return CPATTN_ERR_INVALID_ARG;
-  if (kt == CPATTN_DTYPE_FP8_E4M3) {
+  if (kt != d->dtype && kt != CPATTN_DTYPE_FP8_E4M3 && kt != CPATTN_DTYPE_FP4_E2M1) return CPATTN_ERR_INVALID_ARG;
+  if (kt == CPATTN_DTYPE_FP8_E4M3 || kt == CPATTN_DTYPE_FP4_E2M1) {
     if (d->dtype != CPATTN_DTYPE_BF16) return CPATTN_ERR_UNSUPPORTED_SHAPE;
     const float ks = d->k_descale, vs = d->v_descale;
     if (!(ks > 0.f && ks <= 3.0e38f) || !(vs > 0.f && vs <= 3.0e38f)) return CPATTN_ERR_INVALID_ARG;
   }
-  const int kb = kv_bytes(d);
   if ((d->head_dim * eb) % 16 != 0 || (d->head_dim_v * eb) % 16 != 0) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  if ((d->head_dim * kb) % 16 != 0 || (d->head_dim_v * kb) % 16 != 0) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  if (kt == CPATTN_DTYPE_FP4_E2M1 && (d->head_dim % 32 != 0 || d->head_dim_v % 32 != 0))
+    return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  if (row_bytes(d, d->head_dim) % 16 != 0 || row_bytes(d, d->head_dim_v) % 16 != 0)
+    return CPATTN_ERR_UNSUPPORTED_SHAPE;
   if (d->head_dim_v > d->head_dim) return CPATTN_ERR_UNSUPPORTED_SHAPE;
   return CPATTN_OK;
 }
@@ -72,6 +80,48 @@ struct FusedOut {
   const int32_t* row_order = nullptr;
 };
 
+// A score modification: null, or a cap that is 0 or within [1e-6, 1e30].
+int check_mod(const cpattn_score_mod* m) {
+  if (m == nullptr || m->softcap == 0.f) return CPATTN_OK;
+  return m->softcap >= 1e-6f && m->softcap <= 1e30f ? CPATTN_OK : CPATTN_ERR_INVALID_ARG;
+}
+
+bool modifies(const cpattn_score_mod* m) { return m != nullptr && (m->softcap > 0.f || m->slopes != nullptr); }
+
+WriteArgs write_args(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, const void* k_new, const void* v_new,
+                     const int32_t* positions, const int32_t* qo_indptr, int32_t num_rows, int32_t num_tokens,
+                     const int32_t* kv_page_indptr, const int32_t* kv_page_indices, int32_t* dev_status) {
+  const bool mla = is_mla(desc);
+  const int eb = dtype_bytes(desc->dtype);
+  WriteArgs a;
+  a.pool_k = pool_k;
+  a.pool_v = pool_v;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.positions = positions;
+  a.qo_indptr = qo_indptr;
+  a.page_indptr = kv_page_indptr;
+  a.page_indices = kv_page_indices;
+  a.dev_status = dev_status;
+  a.P = desc->P;
+  a.interleave = interleave_of(desc);
+  a.page_size = desc->page_size;
+  a.num_pages = desc->num_pages;
+  a.num_kv_heads = desc->num_kv_heads;
+  a.num_rows = num_rows;
+  a.num_tokens = num_tokens;
+  a.row_bytes_k = row_bytes(desc, desc->head_dim);
+  a.row_bytes_v = mla ? 0 : row_bytes(desc, desc->head_dim_v);
+  a.src_row_bytes_k = desc->head_dim * eb;
+  a.src_row_bytes_v = mla ? 0 : desc->head_dim_v * eb;
+  a.quant = is_fp4(desc) ? kQuantFp4 : (is_fp8(desc) ? kQuantE4m3 : kQuantNone);
+  a.k_descale = desc->k_descale;
+  a.v_descale = desc->v_descale;
+  a.scale_off_k = pool_rows(desc) * a.row_bytes_k;
+  a.scale_off_v = pool_rows(desc) * a.row_bytes_v;
+  return a;
+}
+
 size_t partial_workspace(const cpattn_pool_desc* desc, int fused, int32_t num_q_heads, int32_t num_tokens,
                          int32_t max_kv_len) {
   if (check_desc(desc) != CPATTN_OK || num_q_heads < 1 || num_tokens < 0 || max_kv_len < 0) return 0;
@@ -87,9 +137,10 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
                 int32_t num_q_heads, int32_t num_rows, int32_t num_tokens, const int32_t* qo_indptr,
                 const int32_t* kv_len, int32_t max_kv_len, const int32_t* kv_page_indptr,
                 const int32_t* kv_page_indices, float scale, float* o_part, float* lse_part, int lse_layout,
-                const FusedOut& f, void* workspace, size_t workspace_bytes, int32_t* dev_status,
-                cudaStream_t stream) {
+                const FusedOut& f, const cpattn_score_mod* mod, void* workspace, size_t workspace_bytes,
+                int32_t* dev_status, cudaStream_t stream) {
   int st = check_desc(desc);
+  if (st == CPATTN_OK) st = check_mod(mod);
   if (st != CPATTN_OK) return st;
   if (num_q_heads < 1 || num_rows < 0 || num_tokens < 0 || max_kv_len < 0) return CPATTN_ERR_INVALID_ARG;
   if (num_q_heads % desc->num_kv_heads != 0) return CPATTN_ERR_INVALID_ARG;
@@ -106,12 +157,13 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   if (!aligned16(pool_k) || !aligned16(pool_v) || !aligned16(q) || !aligned16(o_part) || !aligned16(workspace))
     return CPATTN_ERR_MISALIGNED;
   if (mla && desc->dtype != CPATTN_DTYPE_BF16) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  // E4M3 pools: GQA (the MLA kernel reads bf16 latent rows only)
-  if (is_fp8(desc) && mla) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  // multi-token rows over a bf16 pool: the kernel's copy warps pass pool row
+  // E4M3 and E2M1 pools: GQA (the MLA kernel reads bf16 latent rows only)
+  if ((is_fp8(desc) || is_fp4(desc) || modifies(mod)) && mla) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  // the E2M1 decode kernel keeps pool rows as 32-bit values (2^32 - 1 rows are 137 GB of codes at D 64)
+  if (is_fp4(desc) && pool_rows(desc) >= 0xffffffffLL) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  // multi-token rows over a pool of 16-bit or narrower rows: the kernel's copy warps pass pool row
   // indices as 32-bit values (checked here, before the one-token rows' launch)
-  if (!mla && qo_indptr != nullptr && !is_fp8(desc) &&
-      static_cast<int64_t>(desc->num_pages) * desc->num_kv_heads * desc->page_size >= (int64_t{1} << 31))
+  if (!mla && qo_indptr != nullptr && !is_fp8(desc) && pool_rows(desc) >= (int64_t{1} << 31))
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
 
   PartialPlan plan;
@@ -180,8 +232,15 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.max_chunks = plan.max_chunks;
   a.scale = scale;
   a.kv_fp8 = is_fp8(desc);
+  a.kv_fp4 = is_fp4(desc);
+  a.scale_off = pool_rows(desc) * row_bytes(desc, desc->head_dim);
   a.k_descale = desc->k_descale;
   a.v_descale = desc->v_descale;
+  a.has_mod = modifies(mod);
+  a.softcap = a.has_mod ? mod->softcap : 0.f;
+  a.slopes = a.has_mod ? mod->slopes : nullptr;
+  a.q_pos = a.has_mod ? mod->positions : nullptr;
+  a.q_pos_own = qo_indptr == nullptr;
   a.fused = f.fused;
   a.extra_o = f.extra_o;
   a.extra_lse = f.extra_lse;
@@ -220,8 +279,8 @@ const char* cpattn_status_string(int status) {
 
 size_t cpattn_pool_bytes(const cpattn_pool_desc* d, int which_v) {
   if (check_desc(d) != CPATTN_OK) return 0;
-  const size_t rows = static_cast<size_t>(d->P) * d->num_pages * d->num_kv_heads * (d->page_size / d->P);
-  return rows * (which_v ? d->head_dim_v : d->head_dim) * kv_bytes(d);
+  const int n = which_v ? d->head_dim_v : d->head_dim;
+  return static_cast<size_t>(pool_rows(d)) * (row_bytes(d, n) + (is_fp4(d) ? n / 16 : 0));
 }
 
 int cp_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, const void* k_new, const void* v_new,
@@ -240,33 +299,50 @@ int cp_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, const 
   if (mla && (pool_v != nullptr || v_new != nullptr)) return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(pool_k) || !aligned16(pool_v) || !aligned16(k_new) || !aligned16(v_new))
     return CPATTN_ERR_MISALIGNED;
-  const int eb = dtype_bytes(desc->dtype);
-  WriteArgs a;
-  a.pool_k = pool_k;
-  a.pool_v = pool_v;
-  a.k_new = k_new;
-  a.v_new = v_new;
-  a.positions = positions;
-  a.qo_indptr = qo_indptr;
-  a.page_indptr = kv_page_indptr;
-  a.page_indices = kv_page_indices;
-  a.dev_status = dev_status;
-  a.P = desc->P;
-  a.interleave = interleave_of(desc);
-  a.page_size = desc->page_size;
-  a.num_pages = desc->num_pages;
-  a.num_kv_heads = desc->num_kv_heads;
-  a.num_rows = num_rows;
-  a.num_tokens = num_tokens;
-  const int kb = kv_bytes(desc);
-  a.row_bytes_k = desc->head_dim * kb;
-  a.row_bytes_v = mla ? 0 : desc->head_dim_v * kb;
-  a.src_row_bytes_k = desc->head_dim * eb;
-  a.src_row_bytes_v = mla ? 0 : desc->head_dim_v * eb;
-  a.quant_fp8 = is_fp8(desc);
-  a.k_descale = desc->k_descale;
-  a.v_descale = desc->v_descale;
+  const WriteArgs a = write_args(desc, pool_k, pool_v, k_new, v_new, positions, qo_indptr, num_rows, num_tokens,
+                                 kv_page_indptr, kv_page_indices, dev_status);
   return launch_kv_write(a, stream) == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
+int cp_rope_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, const void* q, const void* k_new,
+                     const void* v_new, int32_t num_q_heads, const int32_t* positions, const int32_t* qo_indptr,
+                     int32_t num_rows, int32_t num_tokens, const int32_t* kv_page_indptr,
+                     const int32_t* kv_page_indices, const float* cos_sin, int32_t table_len, int32_t rot_begin,
+                     int32_t rot_dim, int32_t style, void* q_out, void* k_out, int32_t* dev_status,
+                     cudaStream_t stream) {
+  const int st = check_desc(desc);
+  if (st != CPATTN_OK) return st;
+  if (num_rows < 0 || num_tokens < 0 || table_len < 1) return CPATTN_ERR_INVALID_ARG;
+  if (style != CPATTN_ROPE_HALVES && style != CPATTN_ROPE_PAIRS) return CPATTN_ERR_INVALID_ARG;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || rot_begin < 0 || rot_begin > desc->head_dim - rot_dim)
+    return CPATTN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && num_q_heads < 1)) return CPATTN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return CPATTN_OK;
+  const bool mla = is_mla(desc);
+  if (pool_k == nullptr || k_new == nullptr || positions == nullptr || qo_indptr == nullptr ||
+      kv_page_indptr == nullptr || kv_page_indices == nullptr || cos_sin == nullptr || num_rows < 1)
+    return CPATTN_ERR_INVALID_ARG;
+  if (!mla && (pool_v == nullptr || v_new == nullptr)) return CPATTN_ERR_INVALID_ARG;
+  if (mla && (pool_v != nullptr || v_new != nullptr)) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned16(pool_k) || !aligned16(pool_v) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q) ||
+      !aligned16(q_out) || !aligned16(k_out) || !aligned16(cos_sin))
+    return CPATTN_ERR_MISALIGNED;
+  RopeArgs a;
+  a.w = write_args(desc, pool_k, pool_v, k_new, v_new, positions, qo_indptr, num_rows, num_tokens, kv_page_indptr,
+                   kv_page_indices, dev_status);
+  a.q = q;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.cos_sin = cos_sin;
+  a.num_q_heads = num_q_heads;
+  a.head_dim = desc->head_dim;
+  a.head_dim_v = mla ? 0 : desc->head_dim_v;
+  a.elem_bytes = dtype_bytes(desc->dtype);
+  a.rot_begin = rot_begin;
+  a.rot_dim = rot_dim;
+  a.pairs = style == CPATTN_ROPE_PAIRS;
+  a.table_len = table_len;
+  return launch_rope_kv_write(a, stream);
 }
 
 size_t cp_paged_attn_workspace_bytes(const cpattn_pool_desc* desc, int32_t num_q_heads, int32_t num_tokens,
@@ -287,7 +363,7 @@ int cp_paged_attn_partial(const cpattn_pool_desc* desc, const void* pool_k, cons
   FusedOut none;
   return run_partial(desc, pool_k, pool_v, q, num_q_heads, num_rows, num_tokens, qo_indptr, kv_len, max_kv_len,
                      kv_page_indptr, kv_page_indices, scale, o_part, lse_part, CPATTN_LSE_TOKEN_MAJOR, none,
-                     workspace, workspace_bytes, dev_status, stream);
+                     nullptr, workspace, workspace_bytes, dev_status, stream);
 }
 
 int cp_paged_attn_partial_ex(const cpattn_pool_desc* desc, const void* pool_k, const void* pool_v, const void* q,
@@ -296,10 +372,21 @@ int cp_paged_attn_partial_ex(const cpattn_pool_desc* desc, const void* pool_k, c
                              const int32_t* kv_page_indices, float scale, float* o_part, float* lse_part,
                              int32_t lse_layout, const int32_t* row_order, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, cudaStream_t stream) {
+  return cp_paged_attn_partial_mod(desc, pool_k, pool_v, q, num_q_heads, num_rows, num_tokens, qo_indptr, kv_len,
+                                   max_kv_len, kv_page_indptr, kv_page_indices, scale, o_part, lse_part, lse_layout,
+                                   row_order, nullptr, workspace, workspace_bytes, dev_status, stream);
+}
+
+int cp_paged_attn_partial_mod(const cpattn_pool_desc* desc, const void* pool_k, const void* pool_v, const void* q,
+                              int32_t num_q_heads, int32_t num_rows, int32_t num_tokens, const int32_t* qo_indptr,
+                              const int32_t* kv_len, int32_t max_kv_len, const int32_t* kv_page_indptr,
+                              const int32_t* kv_page_indices, float scale, float* o_part, float* lse_part,
+                              int32_t lse_layout, const int32_t* row_order, const cpattn_score_mod* mod,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream) {
   FusedOut none;
   none.row_order = qo_indptr == nullptr ? row_order : nullptr;
   return run_partial(desc, pool_k, pool_v, q, num_q_heads, num_rows, num_tokens, qo_indptr, kv_len, max_kv_len,
-                     kv_page_indptr, kv_page_indices, scale, o_part, lse_part, lse_layout, none, workspace,
+                     kv_page_indptr, kv_page_indices, scale, o_part, lse_part, lse_layout, none, mod, workspace,
                      workspace_bytes, dev_status, stream);
 }
 
@@ -310,6 +397,18 @@ int cp_paged_attn_fused(const cpattn_pool_desc* desc, const void* pool_k, const 
                         const float* extra_o, const float* extra_lse,
                         int32_t out_dtype, void* out, float* lse_out, void* workspace, size_t workspace_bytes,
                         int32_t* dev_status, cudaStream_t stream) {
+  return cp_paged_attn_fused_mod(desc, pool_k, pool_v, q, num_q_heads, num_rows, num_tokens, qo_indptr, kv_len,
+                                 max_kv_len, kv_page_indptr, kv_page_indices, row_order, scale, extra_o, extra_lse,
+                                 out_dtype, out, lse_out, nullptr, workspace, workspace_bytes, dev_status, stream);
+}
+
+int cp_paged_attn_fused_mod(const cpattn_pool_desc* desc, const void* pool_k, const void* pool_v, const void* q,
+                            int32_t num_q_heads, int32_t num_rows, int32_t num_tokens, const int32_t* qo_indptr,
+                            const int32_t* kv_len, int32_t max_kv_len, const int32_t* kv_page_indptr,
+                            const int32_t* kv_page_indices, const int32_t* row_order, float scale,
+                            const float* extra_o, const float* extra_lse, int32_t out_dtype, void* out, float* lse_out,
+                            const cpattn_score_mod* mod, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            cudaStream_t stream) {
   const int st = check_desc(desc);
   if (st != CPATTN_OK) return st;
   if (out_dtype != CPATTN_DTYPE_BF16 && out_dtype != CPATTN_DTYPE_FP32) return CPATTN_ERR_INVALID_ARG;
@@ -326,7 +425,7 @@ int cp_paged_attn_fused(const cpattn_pool_desc* desc, const void* pool_k, const 
   f.lse_out = lse_out;
   f.row_order = qo_indptr == nullptr ? row_order : nullptr;
   return run_partial(desc, pool_k, pool_v, q, num_q_heads, num_rows, num_tokens, qo_indptr, kv_len, max_kv_len,
-                     kv_page_indptr, kv_page_indices, scale, nullptr, nullptr, CPATTN_LSE_TOKEN_MAJOR, f, workspace,
+                     kv_page_indptr, kv_page_indices, scale, nullptr, nullptr, CPATTN_LSE_TOKEN_MAJOR, f, mod, workspace,
                      workspace_bytes, dev_status, stream);
 }
 
@@ -334,13 +433,23 @@ int own_token_attn(const void* q, const void* k_new, const void* v_new, int32_t 
                    int32_t head_dim, int32_t head_dim_v, int32_t dtype, const int32_t* qo_indptr,
                    int32_t num_rows_bucket, int32_t num_real_rows, int32_t num_tokens, int32_t max_q_len,
                    float scale, float* o_own, float* lse_own, cudaStream_t stream) {
+  return own_token_attn_mod(q, k_new, v_new, num_q_heads, num_kv_heads, head_dim, head_dim_v, dtype, qo_indptr,
+                            num_rows_bucket, num_real_rows, num_tokens, max_q_len, scale, nullptr, o_own, lse_own,
+                            stream);
+}
+
+int own_token_attn_mod(const void* q, const void* k_new, const void* v_new, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t head_dim_v, int32_t dtype, const int32_t* qo_indptr,
+                       int32_t num_rows_bucket, int32_t num_real_rows, int32_t num_tokens, int32_t max_q_len,
+                       float scale, const cpattn_score_mod* mod, float* o_own, float* lse_own, cudaStream_t stream) {
   const int eb = dtype_bytes(dtype);
   if (eb == 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || num_tokens < 0 ||
       num_rows_bucket < 1 || num_real_rows < 0 || num_real_rows > num_rows_bucket || max_q_len < 0)
     return CPATTN_ERR_INVALID_ARG;
   // MLA: one latent head, keys of 576 values whose first 512 are the value (v_new NULL)
   const bool mla = num_kv_heads == 1 && head_dim == 576 && head_dim_v == 512;
-  if (mla ? (dtype != CPATTN_DTYPE_BF16 || v_new != nullptr) : head_dim != head_dim_v)
+  if (check_mod(mod) != CPATTN_OK) return CPATTN_ERR_INVALID_ARG;
+  if (mla ? (dtype != CPATTN_DTYPE_BF16 || v_new != nullptr || modifies(mod)) : head_dim != head_dim_v)
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
   if (num_tokens == 0) return CPATTN_OK;
   if (q == nullptr || k_new == nullptr || qo_indptr == nullptr || o_own == nullptr || lse_own == nullptr)
@@ -362,6 +471,9 @@ int own_token_attn(const void* q, const void* k_new, const void* v_new, int32_t 
   a.num_tokens = num_tokens;
   a.max_q_len = max_q_len;
   a.scale = scale;
+  a.has_mod = modifies(mod);
+  a.softcap = a.has_mod ? mod->softcap : 0.f;
+  a.slopes = a.has_mod ? mod->slopes : nullptr;
   cudaError_t err = cudaSuccess;
   return launch_own_token(a, dtype == CPATTN_DTYPE_BF16, stream, &err);
 }

@@ -67,9 +67,10 @@ struct GqaLaneState {
   // space the generic pointer reaches).  All lanes of the warp must call this
   // together (shuffles); "valid" masks the key of this lane group.  The value
   // row is not touched for an invalid key, so unwritten (NaN) slots never mix
-  // into the output.
-  template <bool kGlobal>
-  __device__ __forceinline__ void step(const uint8_t* krow, const uint8_t* vrow, bool valid) {
+  // into the output.  score(x, g) gives the log2-domain score of head g from
+  // the dot product of its loaded query.
+  template <bool kGlobal, class Score>
+  __device__ __forceinline__ void step(const uint8_t* krow, const uint8_t* vrow, bool valid, Score score) {
     float s[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) s[g] = 0.f;
@@ -102,6 +103,7 @@ struct GqaLaneState {
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        s[g] = score(s[g], g);
         if (s[g] > m[g]) {  // new running max: rescale (rare after the first keys)
           const float alpha = exp2f(m[g] - s[g]);
           l[g] *= alpha;

@@ -11,27 +11,9 @@
 // One thread moves one 16-byte chunk of one (token, KV head) row; the chunks of
 // a row are adjacent threads, so both the read of k_new and the write into the
 // pool are coalesced 16-byte accesses.
-#include "common.cuh"
-#include "launch.h"
+#include "kv_quant.cuh"
 
 namespace cpattn {
-
-// E4M3 code of a float32 value, rounded once to the nearest E4M3 value (ties
-// to the even code), magnitudes of 448 and more (and infinities) saturated to
-// 448, NaN to 0x7F.  Written from the format: normal codes are the float32
-// exponent rebiased from 127 to 7 and the mantissa rounded to 3 bits;
-// below 2^-6 the codes are the multiples m * 2^-9 (m = 0..8).
-__device__ __forceinline__ uint32_t e4m3_rn_satfinite(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t sign = (u >> 24) & 0x80u;
-  const float ax = fabsf(x);
-  if (ax != ax) return 0x7Fu;
-  if (ax >= 448.f) return sign | 0x7Eu;
-  if (ax < 0.015625f) return sign | static_cast<uint32_t>(__float2int_rn(ax * 512.f));  // exact scaling
-  const uint32_t bits = u & 0x7fffffffu;
-  const uint32_t r = (bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20;  // exponent | 3 mantissa bits, to nearest even
-  return sign | (r - ((127u - 7u) << 3));
-}
 
 // E4M3 codes of 16 bf16 values (byte offset src_off of src, chunk c) divided
 // by the descale: IEEE float32 quotient, then e4m3_rn_satfinite.
@@ -58,6 +40,21 @@ __device__ __forceinline__ void store_fp8_chunk(const void* src, int64_t src_off
   *(reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + dst_off) + c) = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// Block c (16 values) of one E2M1 row of nblk blocks from 16 bf16 values.
+__device__ __forceinline__ void store_fp4_block(const void* src, int64_t src_off, void* pool, int64_t scale_off,
+                                                int64_t prow, int nblk, int c, float descale) {
+  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + src_off) + 2 * c;
+  float x[16];
+  Chunk16<__nv_bfloat16>::widen(__ldg(s), x);
+  Chunk16<__nv_bfloat16>::widen(__ldg(s + 1), x + 8);
+  uint2 codes;
+  uint32_t scale;
+  fp4_encode_block(x, descale, codes, scale);
+  uint8_t* p = static_cast<uint8_t*>(pool);
+  *reinterpret_cast<uint2*>(p + (prow * nblk + c) * 8) = codes;
+  p[scale_off + prow * nblk + c] = static_cast<uint8_t>(scale);
+}
+
 __global__ void __launch_bounds__(256) kv_write_kernel(const WriteArgs a, int chunks_per_row) {
   pdl_trigger();
   pdl_wait();
@@ -70,35 +67,24 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const WriteArgs a, int ch
   const int h = rem / chunks_per_row;
   const int c = rem - h * chunks_per_row;
 
-  const int end = __ldg(a.qo_indptr + a.num_rows);
-  if (t >= end) return;  // padding token past the last row
+  const int b = row_of_token(a.qo_indptr, a.num_rows, t);
+  if (b < 0) return;  // padding token past the last row
   const int pos = __ldg(a.positions + t);
   if (pos < 0) return;  // padding token
-  const int b = find_row(a.qo_indptr, a.num_rows, t);
-
-  const int page_idx = pos / a.page_size;
-  const int pbeg = __ldg(a.page_indptr + b);
-  const int pend = __ldg(a.page_indptr + b + 1);
-  if (page_idx >= pend - pbeg) {
-    if (c == 0 && h == 0) report(a.dev_status, CPATTN_DEV_POS_PAST_TABLE);
-    return;
-  }
-  const int page = __ldg(a.page_indices + pbeg + page_idx);
-  if (page < 0 || page >= a.num_pages) {
-    if (c == 0 && h == 0) report(a.dev_status, CPATTN_DEV_PAGE_OUT_OF_RANGE);
-    return;
-  }
-  const int off = pos - page_idx * a.page_size;
-  const int run = off / a.interleave;
-  const int partner = run % a.P;
-  const int slot = (run / a.P) * a.interleave + (off - run * a.interleave);
-  const int ps_l = a.page_size / a.P;
-  // row index inside the pool tensor [P][num_pages][H][ps_l]
-  const int64_t prow =
-      ((static_cast<int64_t>(partner) * a.num_pages + page) * a.num_kv_heads + h) * ps_l + slot;
+  const int64_t row0 = pool_row0(a, b, pos, c == 0 && h == 0);
+  if (row0 < 0) return;
+  const int64_t prow = row0 + static_cast<int64_t>(h) * (a.page_size / a.P);
   const int64_t srow = static_cast<int64_t>(t) * a.num_kv_heads + h;
 
-  if (a.quant_fp8) {
+  if (a.quant == kQuantFp4) {
+    // a block of 16 values: 8 bytes of codes, one scale behind the pool's codes
+    const int nblk_k = a.row_bytes_k / 8, nblk_v = a.row_bytes_v / 8;
+    if (c < nblk_k) store_fp4_block(a.k_new, srow * a.src_row_bytes_k, a.pool_k, a.scale_off_k, prow, nblk_k, c, a.k_descale);
+    if (a.pool_v != nullptr && c < nblk_v)
+      store_fp4_block(a.v_new, srow * a.src_row_bytes_v, a.pool_v, a.scale_off_v, prow, nblk_v, c, a.v_descale);
+    return;
+  }
+  if (a.quant == kQuantE4m3) {
     // 16 codes of the pool row from 16 bf16 values of the new row
     if (c * 16 < a.row_bytes_k) store_fp8_chunk(a.k_new, srow * a.src_row_bytes_k, a.pool_k, prow * a.row_bytes_k, c,
                                                a.k_descale);
@@ -122,7 +108,7 @@ __global__ void __launch_bounds__(256) kv_write_kernel(const WriteArgs a, int ch
 
 cudaError_t launch_kv_write(const WriteArgs& a, cudaStream_t s) {
   const int rb = a.row_bytes_k > a.row_bytes_v ? a.row_bytes_k : a.row_bytes_v;
-  const int chunks = rb / 16;
+  const int chunks = a.quant == kQuantFp4 ? rb / 8 : rb / 16;  // E2M1: one thread a block of 16 values
   const int64_t total = static_cast<int64_t>(a.num_tokens) * a.num_kv_heads * chunks;
   if (total == 0) return cudaSuccess;
   const int threads = 256;

@@ -37,10 +37,25 @@ struct WriteArgs {
   int P, interleave, page_size, num_pages, num_kv_heads, num_rows, num_tokens;
   int row_bytes_k, row_bytes_v;  // bytes of one head's K / V row in the pool
   int src_row_bytes_k, src_row_bytes_v;  // ... in k_new / v_new
-  int quant_fp8;                 // pool holds E4M3 codes of x / descale
+  int quant;                     // kQuant*: pool rows are copies, or codes of x / descale
   float k_descale, v_descale;
+  int64_t scale_off_k, scale_off_v;  // E2M1 pools: byte offset of the block scales (behind every row's codes)
 };
+enum : int { kQuantNone = 0, kQuantE4m3 = 1, kQuantFp4 = 2 };
 cudaError_t launch_kv_write(const WriteArgs& a, cudaStream_t s);
+
+// cp_rope_kv_write: the rotation beside the write's arguments (w.k_new / w.v_new
+// are the new rows, w.pool_v null for MLA).
+struct RopeArgs {
+  WriteArgs w;
+  const void* q;        // null: keys only
+  void* q_out;
+  void* k_out;          // null: the pool only
+  const float* cos_sin; // [table_len][rot_dim]: rot_dim / 2 cosines, then the sines
+  int num_q_heads, head_dim, head_dim_v, elem_bytes;
+  int rot_begin, rot_dim, pairs, table_len;
+};
+int launch_rope_kv_write(const RopeArgs& a, cudaStream_t s);
 
 struct MergeArgs {
   int num_partials;
@@ -99,6 +114,8 @@ struct PartialArgs {
   int max_chunks;  // chunks per (token, partner, kv head), = grid.x
   float scale;
   int kv_fp8;                 // pool holds E4M3 codes: key = code * k_descale, value = code * v_descale
+  int kv_fp4;                 // pool holds E2M1 codes with a scale per 16 values, times the descales
+  int64_t scale_off;          // E2M1: byte offset of the block scales behind the codes (K and V pools alike)
   float k_descale, v_descale;
   // fused calls: o_part / lse_part point into the workspace, and the last
   // partner to finish a (token, KV head) writes the merged output
@@ -108,6 +125,13 @@ struct PartialArgs {
   void* out;               // [T][Hq][Dv], bf16 when out_bf16 else fp32
   int out_bf16;
   float* lse_out;          // [T][Hq] or null
+  // score modification (has_mod): s = scale q.k, capped by softcap * tanh(s / softcap)
+  // when softcap > 0, plus slopes[query head] * (key position - query position)
+  int has_mod;
+  float softcap;
+  const float* slopes;     // [Hq], or null: no distance term
+  const int32_t* q_pos;    // [T] position of each query token, or null: from kv_len
+  int q_pos_own;           // q_pos null: 1 when kv_len counts the query's own key (one token a row)
   // dispatch order of the grid's row axis (a permutation, e.g. longest rows
   // first so the last wave holds the short ones), or null: natural order.
   // Used where the grid's z axis walks rows (one token a row); ignored by
@@ -130,7 +154,9 @@ bool plan_partial(int mla, int fused, int P, int interleave, int page_size, int 
 int launch_gqa_partial(const PartialArgs& a, int dtype_bf16, cudaStream_t s, cudaError_t* err);
 int launch_gqa_partial_mma(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
 int launch_gqa_partial_ext(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
-int launch_gqa_partial_ext_ws(const PartialArgs& a, cudaStream_t s, cudaError_t* err);  // bf16 and E4M3 pools
+int launch_gqa_partial_ext_bf16(const PartialArgs& a, cudaStream_t s, cudaError_t* err);  // by pool type
+int launch_gqa_partial_ext_e4m3(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
+int launch_gqa_partial_ext_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
 int launch_mla_partial(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
 // MLA kernel: workspace slots for the pieces of cut stripes (0: no stripe can be
 // cut); `grouped`: fused calls whose tiles are logical pages (cut tokens)
@@ -146,9 +172,13 @@ struct OwnArgs {
   const int32_t* qo_indptr;
   int num_q_heads, num_kv_heads, head_dim, num_rows_bucket, num_real_rows, num_tokens, max_q_len;
   float scale;
+  int has_mod;          // as in PartialArgs
+  float softcap;
+  const float* slopes;  // [Hq] or null
 };
 int launch_own_token(const OwnArgs& a, int dtype_bf16, cudaStream_t s, cudaError_t* err);
 int launch_own_token_mma(const OwnArgs& a, cudaStream_t s, cudaError_t* err);  // bf16, tensor cores
 int launch_gqa_partial_mmat(const PartialArgs& a, cudaStream_t s, cudaError_t* err);  // decode rows, groups <= 8
+int launch_gqa_partial_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err);   // decode rows, E2M1 pools
 
 }  // namespace cpattn

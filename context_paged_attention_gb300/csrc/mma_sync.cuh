@@ -101,4 +101,23 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16) {
   return pack_bf16(f.x, f.y);
 }
 
+// Two E2M1 codes (low half first) of byte i of w -> float16 pair (exact).
+template <int i>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b%2;\n}\n"
+      : "=r"(r)
+      : "r"(w), "n"(i));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// float16 pair -> bf16 pair (nearest even; exact for at most 8 significant bits).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16(f.x, f.y);
+}
+
 }  // namespace cpattn

@@ -17,7 +17,8 @@ namespace cpattn {
 
 constexpr int kOwnWarps = 4;
 
-template <typename T, int D, int G>
+// MOD: modified scores (score_mod.cuh), with the accurate tanhf.
+template <typename T, int D, int G, bool MOD>
 __global__ void __launch_bounds__(kOwnWarps * 32) own_token_kernel(const OwnArgs a) {
   using C = GqaCfg<T, D, G>;
   constexpr int NW = kOwnWarps;
@@ -36,7 +37,10 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_token_kernel(const OwnArgs
   GqaLaneState<T, D, G> st;
   st.init(lane);
   st.load_q(static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + h * G) * C::ROWB, real,
-            a.scale * kLog2e);
+            a.scale * (MOD ? 1.f : kLog2e));
+  float slope[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) slope[g] = MOD && a.slopes != nullptr ? __ldg(a.slopes + h * G + g) : 0.f;
 
   if (real) {
     const int64_t stride = static_cast<int64_t>(a.num_kv_heads) * C::ROWB;
@@ -46,7 +50,15 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_token_kernel(const OwnArgs
       const int j = base + st.grp;
       const bool valid = j <= t;
       const int jj = valid ? j : t;
-      st.template step<true>(kb + jj * stride, vb + jj * stride, valid);
+      if constexpr (MOD) {
+        const float away = static_cast<float>(jj - t);
+        st.template step<true>(kb + jj * stride, vb + jj * stride, valid, [&](float x, int g) {
+          if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+          return fmaf(slope[g], away, x) * kLog2e;
+        });
+      } else {
+        st.template step<true>(kb + jj * stride, vb + jj * stride, valid, [](float x, int) { return x; });
+      }
     }
   }
   st.merge_groups();
@@ -63,21 +75,21 @@ __global__ void __launch_bounds__(kOwnWarps * 32) own_token_kernel(const OwnArgs
   }
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool MOD>
 static int launch_own_t(const OwnArgs& a, cudaStream_t s, cudaError_t* err) {
   dim3 grid(a.num_tokens, a.num_kv_heads);
-  own_token_kernel<T, D, G><<<grid, kOwnWarps * 32, 0, s>>>(a);
+  own_token_kernel<T, D, G, MOD><<<grid, kOwnWarps * 32, 0, s>>>(a);
   *err = cudaGetLastError();
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 static int own_dispatch_g(const OwnArgs& a, int G, cudaStream_t s, cudaError_t* err) {
   switch (G) {
-    case 1: return launch_own_t<T, D, 1>(a, s, err);
-    case 2: return launch_own_t<T, D, 2>(a, s, err);
-    case 4: return launch_own_t<T, D, 4>(a, s, err);
-    case 8: return launch_own_t<T, D, 8>(a, s, err);
+    case 1: return launch_own_t<T, D, 1, MOD>(a, s, err);
+    case 2: return launch_own_t<T, D, 2, MOD>(a, s, err);
+    case 4: return launch_own_t<T, D, 4, MOD>(a, s, err);
+    case 8: return launch_own_t<T, D, 8, MOD>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
 }
@@ -153,8 +165,10 @@ int launch_own_token(const OwnArgs& a, int dtype_bf16, cudaStream_t s, cudaError
   if (dtype_bf16) {
     return launch_own_token_mma(a, s, err);  // tensor cores (own_token_mma.cu)
   } else {
-    if (a.head_dim == 128) return own_dispatch_g<float, 128>(a, G, s, err);
-    if (a.head_dim == 64) return own_dispatch_g<float, 64>(a, G, s, err);
+    if (a.head_dim == 128)
+      return a.has_mod ? own_dispatch_g<float, 128, true>(a, G, s, err) : own_dispatch_g<float, 128, false>(a, G, s, err);
+    if (a.head_dim == 64)
+      return a.has_mod ? own_dispatch_g<float, 64, true>(a, G, s, err) : own_dispatch_g<float, 64, false>(a, G, s, err);
   }
   return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }

@@ -18,6 +18,7 @@
 // and tokens past the last row get O = 0, LSE = -inf without any K/V read.
 #include "launch.h"
 #include "mma_sync.cuh"
+#include "score_mod.cuh"
 
 namespace cpattn {
 
@@ -27,7 +28,8 @@ constexpr int kOwnKeys = 16;
 constexpr int kOwnStages = 3;
 }  // namespace
 
-template <int D, int G>
+// MOD: modified scores (score_mod.cuh).
+template <int D, int G, bool MOD>
 __global__ void __launch_bounds__(kOwnMmaWarps * 32) own_token_mma_kernel(const OwnArgs a) {
   constexpr int NW = kOwnMmaWarps;
   constexpr int KT = kOwnKeys;
@@ -130,7 +132,16 @@ __global__ void __launch_bounds__(kOwnMmaWarps * 32) own_token_mma_kernel(const 
 #pragma unroll
     for (int u = 0; u < NT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    const float sl = a.scale * kLog2e;
+    const float sl = a.scale * (MOD ? 1.f : kLog2e);
+    ScoreMod smod;
+    float slope0 = 0.f, slope1 = 0.f;
+    if constexpr (MOD) {
+      smod = score_mod_of(a.softcap);
+      if (a.slopes != nullptr) {
+        slope0 = __ldg(a.slopes + h * G + quad % G);
+        slope1 = __ldg(a.slopes + h * G + (quad + 8) % G);
+      }
+    }
     const int mrow = lane & 7;
     const int mi = lane >> 3;
     const int pos0 = tok0 - r0, pos1 = tok1 - r0;  // causal limits (key index <= position)
@@ -170,8 +181,13 @@ __global__ void __launch_bounds__(kOwnMmaWarps * 32) own_token_mma_kernel(const 
             const int kj = i * KT + j * 8 + 2 * qi + e;
             const bool v0 = ok0 && kj <= pos0;
             const bool v1 = ok1 && kj <= pos1;
-            s[j][e] = v0 ? (s[j][e] + s_alt[j][e]) * sl : -INFINITY;
-            s[j][e + 2] = v1 ? (s[j][e + 2] + s_alt[j][e + 2]) * sl : -INFINITY;
+            float x0 = (s[j][e] + s_alt[j][e]) * sl, x1 = (s[j][e + 2] + s_alt[j][e + 2]) * sl;
+            if constexpr (MOD) {
+              x0 = mod_score(smod, x0, slope0, static_cast<float>(kj - pos0));
+              x1 = mod_score(smod, x1, slope1, static_cast<float>(kj - pos1));
+            }
+            s[j][e] = v0 ? x0 : -INFINITY;
+            s[j][e + 2] = v1 ? x1 : -INFINITY;
             bm0 = fmaxf(bm0, s[j][e]);
             bm1 = fmaxf(bm1, s[j][e + 2]);
           }
@@ -260,11 +276,11 @@ __global__ void __launch_bounds__(kOwnMmaWarps * 32) own_token_mma_kernel(const 
   }
 }
 
-template <int D, int G>
+template <int D, int G, bool MOD>
 static int launch_own_mma_t(const OwnArgs& a, cudaStream_t s, cudaError_t* err) {
   constexpr int TQ = kOwnMmaWarps * (16 / G);
   const size_t smem = static_cast<size_t>(kOwnStages) * kOwnKeys * D * 2 * 2;
-  auto kern = own_token_mma_kernel<D, G>;
+  auto kern = own_token_mma_kernel<D, G, MOD>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
@@ -275,17 +291,23 @@ static int launch_own_mma_t(const OwnArgs& a, cudaStream_t s, cudaError_t* err) 
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-int launch_own_token_mma(const OwnArgs& a, cudaStream_t s, cudaError_t* err) {
-  const int G = a.num_q_heads / a.num_kv_heads;
-  if (a.head_dim != 128 && a.head_dim != 64) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+template <int D, bool MOD>
+static int own_mma_dispatch_g(const OwnArgs& a, int G, cudaStream_t s, cudaError_t* err) {
   switch (G) {
-    case 1: return a.head_dim == 128 ? launch_own_mma_t<128, 1>(a, s, err) : launch_own_mma_t<64, 1>(a, s, err);
-    case 2: return a.head_dim == 128 ? launch_own_mma_t<128, 2>(a, s, err) : launch_own_mma_t<64, 2>(a, s, err);
-    case 4: return a.head_dim == 128 ? launch_own_mma_t<128, 4>(a, s, err) : launch_own_mma_t<64, 4>(a, s, err);
-    case 8: return a.head_dim == 128 ? launch_own_mma_t<128, 8>(a, s, err) : launch_own_mma_t<64, 8>(a, s, err);
-    case 16: return a.head_dim == 128 ? launch_own_mma_t<128, 16>(a, s, err) : launch_own_mma_t<64, 16>(a, s, err);
+    case 1: return launch_own_mma_t<D, 1, MOD>(a, s, err);
+    case 2: return launch_own_mma_t<D, 2, MOD>(a, s, err);
+    case 4: return launch_own_mma_t<D, 4, MOD>(a, s, err);
+    case 8: return launch_own_mma_t<D, 8, MOD>(a, s, err);
+    case 16: return launch_own_mma_t<D, 16, MOD>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
+}
+
+int launch_own_token_mma(const OwnArgs& a, cudaStream_t s, cudaError_t* err) {
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (a.head_dim == 128) return a.has_mod ? own_mma_dispatch_g<128, true>(a, G, s, err) : own_mma_dispatch_g<128, false>(a, G, s, err);
+  if (a.head_dim == 64) return a.has_mod ? own_mma_dispatch_g<64, true>(a, G, s, err) : own_mma_dispatch_g<64, false>(a, G, s, err);
+  return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }
 
 }  // namespace cpattn

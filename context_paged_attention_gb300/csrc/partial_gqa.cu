@@ -17,6 +17,7 @@
 // chunks is finished by the last CTA to arrive (split_combine.cuh).
 #include "gqa_core.cuh"
 #include "launch.h"
+#include "score_mod.cuh"
 #include "split_combine.cuh"
 
 namespace cpattn {
@@ -25,7 +26,9 @@ constexpr int kGqaWarps = 4;
 constexpr int kGqaStages = 6;
 constexpr int kSegMax = 8;
 
-template <typename T, int D, int G>
+// MOD: modified scores (score_mod.cuh), with the accurate tanhf: this path is
+// held to float32.
+template <typename T, int D, int G, bool MOD>
 __global__ void __launch_bounds__(kGqaWarps * 32) gqa_partial_kernel(const PartialArgs a) {
   using C = GqaCfg<T, D, G>;
   constexpr int NW = kGqaWarps;
@@ -69,7 +72,15 @@ __global__ void __launch_bounds__(kGqaWarps * 32) gqa_partial_kernel(const Parti
   GqaLaneState<T, D, G> st;
   st.init(lane);
   st.load_q(static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(t) * a.num_q_heads + h * G) * C::ROWB,
-            b >= 0, a.scale * kLog2e);
+            b >= 0, a.scale * (MOD ? 1.f : kLog2e));
+  float slope[G];
+  int qpos = 0;
+  if constexpr (MOD) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) slope[g] = a.slopes != nullptr ? __ldg(a.slopes + h * G + g) : 0.f;
+    if (a.slopes != nullptr && b >= 0)
+      qpos = query_pos(a, b, t, a.qo_indptr != nullptr ? __ldg(a.qo_indptr + b) : t);
+  }
 
   const int32_t* pages = nullptr;
   int npages = 0;
@@ -135,7 +146,15 @@ __global__ void __launch_bounds__(kGqaWarps * 32) gqa_partial_kernel(const Parti
       const int tk = base + st.grp;
       const bool valid = seg_ok && tk < n;
       const int row = valid ? tk : 0;
-      st.template step<false>(sk + row * C::ROWB, sv + row * C::ROWB, valid);
+      if constexpr (MOD) {
+        const float away = static_cast<float>(stripe_pos(k0 + tk, p, P, a.interleave) - qpos);
+        st.template step<false>(sk + row * C::ROWB, sv + row * C::ROWB, valid, [&](float x, int g) {
+          if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+          return fmaf(slope[g], away, x) * kLog2e;
+        });
+      } else {
+        st.template step<false>(sk + row * C::ROWB, sv + row * C::ROWB, valid, [](float x, int) { return x; });
+      }
     }
   }
   cp_async_wait<0>();
@@ -173,13 +192,13 @@ __global__ void __launch_bounds__(kGqaWarps * 32) gqa_partial_kernel(const Parti
   if (a.fused) pair_finish(a, t, h, G, D, sm, scratch_cap);
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool MOD>
 static int launch_gqa_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   using C = GqaCfg<T, D, G>;
   const size_t ring = static_cast<size_t>(kGqaWarps) * kGqaStages * a.seg * C::ROWB * 2;
   const size_t comb = GqaLaneState<T, D, G>::merge_smem_bytes(kGqaWarps);
   const size_t smem = ring > comb ? ring : comb;
-  auto kern = gqa_partial_kernel<T, D, G>;
+  auto kern = gqa_partial_kernel<T, D, G, MOD>;
   if (smem > 32 * 1024) {  // the kernel also has a little static shared memory
     static std::atomic<int> smem_set[64];
     *err = ensure_smem(kern, smem, smem_set);
@@ -191,13 +210,13 @@ static int launch_gqa_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) 
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 static int dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
   switch (G) {
-    case 1: return launch_gqa_t<T, D, 1>(a, s, err);
-    case 2: return launch_gqa_t<T, D, 2>(a, s, err);
-    case 4: return launch_gqa_t<T, D, 4>(a, s, err);
-    case 8: return launch_gqa_t<T, D, 8>(a, s, err);
+    case 1: return launch_gqa_t<T, D, 1, MOD>(a, s, err);
+    case 2: return launch_gqa_t<T, D, 2, MOD>(a, s, err);
+    case 4: return launch_gqa_t<T, D, 4, MOD>(a, s, err);
+    case 8: return launch_gqa_t<T, D, 8, MOD>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
 }
@@ -208,8 +227,8 @@ int launch_gqa_partial(const PartialArgs& a, int dtype_bf16, cudaStream_t s, cud
   if (dtype_bf16) {
     return launch_gqa_partial_mma(a, s, err);  // bf16 pools: tensor-core path (partial_gqa_mma.cu)
   } else {
-    if (a.head_dim == 128) return dispatch_g<float, 128>(a, G, s, err);
-    if (a.head_dim == 64) return dispatch_g<float, 64>(a, G, s, err);
+    if (a.head_dim == 128) return a.has_mod ? dispatch_g<float, 128, true>(a, G, s, err) : dispatch_g<float, 128, false>(a, G, s, err);
+    if (a.head_dim == 64) return a.has_mod ? dispatch_g<float, 64, true>(a, G, s, err) : dispatch_g<float, 64, false>(a, G, s, err);
   }
   return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }

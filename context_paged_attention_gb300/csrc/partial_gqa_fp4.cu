@@ -1,0 +1,478 @@
+// cp_paged_attn_partial, GQA rows of one token over an E2M1 (4-bit) pool.
+//
+// A pool row holds D codes of 4 bits (value 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with
+// a sign), an E4M3 scale per 16 values, and the tensor's descale: 72 bytes at
+// D 128 where bf16 takes 256.  The work split, partner addressing and split-KV
+// merge are those of the bf16 decode kernel (CTA = chunk of partner p's stripe
+// of row b for KV head h; stripe slot k at page k / (page_size / P), slot
+// k % (page_size / P) -- mstar PR #1124 "Context / Sequence Parallel 1/5",
+// description).
+//
+// Heads on the N side of mma.sync m16n8k16, keys (S^T = K Q^T) and dims
+// (O^T = V^T P^T) on the M side.  The order of the MMA's k index (dims of S,
+// keys of P V) is free as long as both operands follow it, so every lane's
+// codes are consecutive in its row and no ldmatrix is needed:
+//   K: lane (g = lane / 4, q = lane % 4) reads dims [q D/4, (q + 1) D/4) of
+//      keys g and g + 8 with one wide load each; the query fragment follows.
+//   V: the lane reads block g of 16 dims (D 64: half a block) of its four keys
+//      and pairs the codes of two keys by nibble masks, so a byte converts to
+//      the (key, key') operand pair; block g has one scale a key, so the four
+//      scales of a lane serve all of its m-tiles.
+// Codes convert to float16 by cvt (two a instruction) and take their scale in
+// float16: at most 2 + 4 significant bits between 2^-10 and 2688, so the
+// product is exact.  P is rounded to float16 (relative 2^-11 at most, below
+// the bf16 output's 2^-9); its sum and the running max stay in float32.
+//
+// Loads: cp.async, 16 bytes a lane for the codes and one row's scales a lane,
+// stages of 32 keys a warp.
+#include <type_traits>
+
+#include "gqa_core.cuh"
+#include "launch.h"
+#include "mma_sync.cuh"
+#include "score_mod.cuh"
+#include "split_combine.cuh"
+
+namespace cpattn {
+
+namespace {
+constexpr int kF4Warps = 4;
+constexpr int kF4Keys = 32;    // keys a stage
+constexpr int kF4Stages = 2;
+
+template <int D>
+struct F4Smem {
+  static constexpr int ROWB = D / 2;        // code bytes of a row
+  static constexpr int SCB = D / 16;        // scale bytes of a row
+  static constexpr int CODES = kF4Keys * ROWB;
+  static constexpr int SCALES = kF4Keys * SCB;
+  static constexpr int STAGE = 2 * (CODES + SCALES);
+  static constexpr size_t RING = static_cast<size_t>(kF4Warps) * kF4Stages * STAGE;
+};
+
+// stage row of MMA key index r (0..7): the permutation spreads the rows that
+// one phase of the V loads reads over all banks
+__device__ __forceinline__ int f4_row(int r) { return r < 4 ? r : (r ^ 1); }
+// position of 16-byte chunk c of stage row r
+template <int D>
+__device__ __forceinline__ int f4_chunk(int c, int r) {
+  return D == 128 ? c ^ (r & 2) : c;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(void* dst, const void* src) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(src), "n"(BYTES) : "memory");
+}
+}  // namespace
+
+template <int D, int G, bool MOD>
+__global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_kernel(const PartialArgs a) {
+  using SM = F4Smem<D>;
+  constexpr int NW = kF4Warps, KT = kF4Keys, NST = kF4Stages;
+  constexpr int CH = SM::ROWB / 16;        // 16-byte chunks of a row's codes
+  constexpr int ITERS = KT * CH / 32;
+  constexpr int NT = G > 8 ? 2 : 1;        // n-tiles of 8 heads
+  constexpr int MMAS = D / 16;             // k-steps of S^T, m-tiles of O^T
+  constexpr int KW = D / 32;               // code words a lane holds of a key row
+  constexpr int VW = D / 64;               // ... of a value row
+  constexpr uint32_t NOROW = 0xffffffffu;  // the launch checks that rows fit 32 bits
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_vmask[NW][NST];
+
+  const int c = blockIdx.x;
+  const int p = blockIdx.y / a.num_kv_heads;
+  const int h = blockIdx.y - p * a.num_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = a.P;
+  const int g8 = lane >> 2, qi = lane & 3;
+
+  pdl_trigger();
+  pdl_wait();
+  const int b = ordered_row(a.row_order, blockIdx.z, gridDim.z, a.dev_status);
+  if (b < 0) return;
+  int t = b;
+  if (a.qo_indptr != nullptr) {
+    t = __ldg(a.qo_indptr + b);
+    if (__ldg(a.qo_indptr + b + 1) - t != 1) return;
+  }
+  int L = __ldg(a.kv_len + b);
+  if (L > a.max_kv_len) {
+    if (c == 0 && threadIdx.x == 0) report(a.dev_status, CPATTN_DEV_POS_PAST_TABLE);
+    L = a.max_kv_len;
+  }
+  const int n_p = stripe_len(L, p, P, a.interleave);
+  const int nchunks = n_p > 0 ? (n_p + a.chunk - 1) / a.chunk : 1;
+  if (c >= nchunks) return;
+  const int k_begin = c * a.chunk;
+  const int k_end = min(n_p, k_begin + a.chunk);
+  const int nstage = k_end > k_begin ? (k_end - k_begin + KT - 1) / KT : 0;
+  const int my_n = nstage > warp ? (nstage - warp + NW - 1) / NW : 0;
+
+  // Q as the B operand: head g8 (+ 8), dims q D/4 + 4 m .. + 3 of MMA m
+  uint32_t qb[NT][MMAS][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int hd = n * 8 + g8;
+    const bool ok = hd < G;
+    const uint2* qw = reinterpret_cast<const uint2*>(
+        static_cast<const uint8_t*>(a.q) +
+        (static_cast<int64_t>(t) * a.num_q_heads + h * G + (ok ? hd : 0)) * (2 * D) + qi * (D / 2));
+#pragma unroll
+    for (int m = 0; m < MMAS; ++m) {
+      const uint2 w = ok ? __ldg(qw + m) : make_uint2(0u, 0u);
+      qb[n][m][0] = bf16x2_to_f16x2(w.x);
+      qb[n][m][1] = bf16x2_to_f16x2(w.y);
+    }
+  }
+
+  uint8_t* ring = smem + static_cast<size_t>(warp) * NST * SM::STAGE;
+  const uint8_t* poolk = static_cast<const uint8_t*>(a.pool_k);
+  const uint8_t* poolv = static_cast<const uint8_t*>(a.pool_v);
+  const uint8_t* sclk = poolk + a.scale_off;
+  const uint8_t* sclv = poolv + a.scale_off;
+
+  // page ids of the chunk, checked once
+  int* spg = reinterpret_cast<int*>(smem + SM::RING);
+  const int j0 = k_begin / a.ps_l;
+  if (nstage > 0) {
+    const int j1 = (k_end - 1) / a.ps_l;
+    const int pb = __ldg(a.page_indptr + b);
+    const int npages = __ldg(a.page_indptr + b + 1) - pb;
+    for (int x = threadIdx.x; x <= j1 - j0; x += blockDim.x) {
+      const int j = j0 + x;
+      int pg = -1;
+      if (j >= npages) {
+        report(a.dev_status, CPATTN_DEV_POS_PAST_TABLE);
+      } else {
+        pg = __ldg(a.page_indices + pb + j);
+        if (pg < 0 || pg >= a.num_pages) {
+          report(a.dev_status, CPATTN_DEV_PAGE_OUT_OF_RANGE);
+          pg = -1;
+        }
+      }
+      spg[x] = pg;
+    }
+  }
+  __syncthreads();
+  const uint32_t head_row0 = (static_cast<uint32_t>(p) * a.num_pages * a.num_kv_heads + h) * a.ps_l;
+  const uint32_t page_rows = static_cast<uint32_t>(a.num_kv_heads) * a.ps_l;
+
+  // stage i of this warp: lane = key resolves its row and copies its scales,
+  // the codes go 32 consecutive chunks an instruction
+  auto issue = [&](int i) {
+    if (i < my_n) {
+      const int k = k_begin + (warp + i * NW) * KT + lane;
+      uint32_t myrow = NOROW;
+      if (k < k_end) {
+        const int j = page_of_slot(a, k);
+        const int pg = spg[j - j0];
+        if (pg >= 0) myrow = head_row0 + static_cast<uint32_t>(pg) * page_rows + static_cast<uint32_t>(k - j * a.ps_l);
+      }
+      const uint32_t vm = __ballot_sync(0xffffffffu, myrow != NOROW);
+      if (lane == 0) s_vmask[warp][i % NST] = vm;
+      uint8_t* sk = ring + (i % NST) * SM::STAGE;
+      uint8_t* sv = sk + SM::CODES;
+      uint8_t* ssk = sv + SM::CODES + lane * SM::SCB;
+      uint8_t* ssv = ssk + SM::SCALES;
+      if (myrow != NOROW) {
+        cp_async_small<SM::SCB>(ssk, sclk + static_cast<uint64_t>(myrow) * SM::SCB);
+        cp_async_small<SM::SCB>(ssv, sclv + static_cast<uint64_t>(myrow) * SM::SCB);
+      } else {  // a masked key's value is 0, never NaN
+#pragma unroll
+        for (int x = 0; x < SM::SCB; x += 4) *reinterpret_cast<uint32_t*>(ssv + x) = 0u;
+      }
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        const int idx = it * 32 + lane;
+        const int key = idx / CH, ch = idx - key * CH;
+        const uint32_t row = __shfl_sync(0xffffffffu, myrow, key);
+        const int soff = key * SM::ROWB + f4_chunk<D>(ch, key) * 16;
+        if (row != NOROW) {
+          const uint64_t src = static_cast<uint64_t>(row) * SM::ROWB + ch * 16;
+          cp_async16(sk + soff, poolk + src);
+          cp_async16(sv + soff, poolv + src);
+        } else {
+          *reinterpret_cast<uint4*>(sv + soff) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+  float o[NT][MMAS][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int u = 0; u < MMAS; ++u) o[n][u][0] = o[n][u][1] = o[n][u][2] = o[n][u][3] = 0.f;
+  float mx[NT][2], l[NT][2];  // heads 8 n + 2 qi, + 1
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+  const float sl = a.scale * a.k_descale * (MOD ? 1.f : kLog2e);
+  const int krow = f4_row(g8);             // stage rows of keys g8 (+ 8)
+  const int vr0 = f4_row(2 * qi), vr1 = f4_row(2 * qi + 1);
+  ScoreMod sm_mod;
+  float slope[NT][2];
+  int qpos = 0;
+  if constexpr (MOD) {
+    sm_mod = score_mod_of(a.softcap);
+    qpos = a.slopes != nullptr ? query_pos(a, b, t, t) : 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hd = n * 8 + 2 * qi + e;
+        slope[n][e] = a.slopes != nullptr && hd < G ? __ldg(a.slopes + h * G + hd) : 0.f;
+      }
+  }
+
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) issue(i);
+
+  for (int i = 0; i < my_n; ++i) {
+    cp_async_wait<NST - 2>();
+    __syncwarp();
+    issue(i + NST - 1);
+
+    const uint8_t* sk = ring + (i % NST) * SM::STAGE;
+    const uint8_t* sv = sk + SM::CODES;
+    const uint8_t* ssk = sv + SM::CODES;
+    const uint8_t* ssv = ssk + SM::SCALES;
+    const uint32_t vm = s_vmask[warp][i % NST];
+
+    // ---- S^T of the two 16-key tiles
+    float st[2][NT][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) st[u][n][0] = st[u][n][1] = st[u][n][2] = st[u][n][3] = 0.f;
+      uint32_t kw[2][KW], ks[2][KW / 2];  // keys g8, g8 + 8: code words, one scale a pair of words
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = u * 16 + e * 8 + krow;
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sk + r * SM::ROWB + f4_chunk<D>(qi, r) * 16);
+          kw[e][0] = w.x, kw[e][1] = w.y, kw[e][2] = w.z, kw[e][3] = w.w;
+          const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ssk + r * SM::SCB + 2 * qi));
+          ks[e][0] = __byte_perm(s2, 0u, 0x1010u);
+          ks[e][1] = __byte_perm(s2, 0u, 0x3232u);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(sk + r * SM::ROWB + qi * 8);
+          kw[e][0] = w.x, kw[e][1] = w.y;
+          ks[e][0] = __byte_perm(e4m3x2_to_f16x2(ssk[r * SM::SCB + qi]), 0u, 0x1010u);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
+        const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<0>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
+                                mul_f16x2(e2m1x2_to_f16x2<1>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
+        const uint32_t fb[4] = {mul_f16x2(e2m1x2_to_f16x2<2>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
+                                mul_f16x2(e2m1x2_to_f16x2<3>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(st[u][n], fa, qb[n][2 * w][0], qb[n][2 * w][1]);
+          mma_f16(st[u][n], fb, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+        }
+      }
+    }
+    // ---- scores in log2 units, masked; the running max over the 32 keys
+    bool ok[2][2];
+    float away[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = u * 16 + e * 8 + krow;
+        ok[u][e] = (vm >> r) & 1u;
+        if constexpr (MOD)
+          away[u][e] = static_cast<float>(
+              stripe_pos(k_begin + (warp + i * NW) * KT + r, p, P, a.interleave) - qpos);
+      }
+    uint32_t pb[2][NT][2];  // P^T as the B operand
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float bm0 = -INFINITY, bm1 = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x0 = st[u][n][2 * e] * sl, x1 = st[u][n][2 * e + 1] * sl;
+          if constexpr (MOD) {
+            x0 = mod_score(sm_mod, x0, slope[n][0], away[u][e]);
+            x1 = mod_score(sm_mod, x1, slope[n][1], away[u][e]);
+          }
+          x0 = ok[u][e] ? x0 : -INFINITY;
+          x1 = ok[u][e] ? x1 : -INFINITY;
+          st[u][n][2 * e] = x0;
+          st[u][n][2 * e + 1] = x1;
+          bm0 = fmaxf(bm0, x0);
+          bm1 = fmaxf(bm1, x1);
+        }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
+        bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+      }
+      const bool up0 = bm0 > mx[n][0] + 8.f, up1 = bm1 > mx[n][1] + 8.f;
+      if (__any_sync(0xffffffffu, up0 || up1)) {
+        const float a0 = up0 ? exp2f(mx[n][0] - bm0) : 1.f;
+        const float a1 = up1 ? exp2f(mx[n][1] - bm1) : 1.f;
+        if (up0) mx[n][0] = bm0;
+        if (up1) mx[n][1] = bm1;
+        l[n][0] *= a0;
+        l[n][1] *= a1;
+#pragma unroll
+        for (int u = 0; u < MMAS; ++u) {
+          o[n][u][0] *= a0;
+          o[n][u][1] *= a1;
+          o[n][u][2] *= a0;
+          o[n][u][3] *= a1;
+        }
+      }
+      // masked keys: 2^(-inf) = 0; while a head has met no key its max is -inf and 0 stands in
+      const float m0 = mx[n][0] == -INFINITY ? 0.f : mx[n][0];
+      const float m1 = mx[n][1] == -INFINITY ? 0.f : mx[n][1];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p0 = ex2_approx(st[u][n][2 * e] - m0), p1 = ex2_approx(st[u][n][2 * e + 1] - m1);
+          l[n][0] += p0;
+          l[n][1] += p1;
+          uint32_t tr = pack_f16(p0, p1);
+          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;\n" : "+r"(tr));
+          pb[u][n][e] = tr;
+        }
+    }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t vw[4][VW];
+      uint32_t sb[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = u * 16 + (e >> 1) * 8 + ((e & 1) ? vr1 : vr0);
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(sv + r * SM::ROWB + f4_chunk<D>(g8 >> 1, r) * 16 + (g8 & 1) * 8);
+          vw[e][0] = w.x, vw[e][1] = w.y;
+          sb[e] = ssv[r * SM::SCB + g8];
+        } else {
+          vw[e][0] = *reinterpret_cast<const uint32_t*>(sv + r * SM::ROWB + g8 * 4);
+          sb[e] = ssv[r * SM::SCB + (g8 >> 1)];
+        }
+      }
+      const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        constexpr uint32_t LO = 0x0f0f0f0fu;
+        const uint32_t e01 = (vw[0][w] & LO) | ((vw[1][w] << 4) & ~LO), o01 = ((vw[0][w] >> 4) & LO) | (vw[1][w] & ~LO);
+        const uint32_t e23 = (vw[2][w] & LO) | ((vw[3][w] << 4) & ~LO), o23 = ((vw[2][w] >> 4) & LO) | (vw[3][w] & ~LO);
+        auto tile = [&](auto ic) {
+          constexpr int x = decltype(ic)::value;
+          const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<x>(e01), s01), mul_f16x2(e2m1x2_to_f16x2<x>(o01), s01),
+                                  mul_f16x2(e2m1x2_to_f16x2<x>(e23), s23), mul_f16x2(e2m1x2_to_f16x2<x>(o23), s23)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * w + x], fa, pb[u][n][0], pb[u][n][1]);
+        };
+        tile(std::integral_constant<int, 0>{});
+        tile(std::integral_constant<int, 1>{});
+        tile(std::integral_constant<int, 2>{});
+        tile(std::integral_constant<int, 3>{});
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- warp states -> shared memory, cross-warp merge
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
+  __syncthreads();
+  float* sm = reinterpret_cast<float*>(smem);
+  float* sm_o = sm;                 // [NW][G][D]
+  float* sm_m = sm_o + NW * G * D;  // [NW][G]
+  float* sm_l = sm_m + NW * G;      // [NW][G]
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int hd = n * 8 + 2 * qi + e;
+      if (hd < G) {
+        // m-tile u: dims g8 D/8 + 2 u (row g8) and + 1 (row g8 + 8)
+        float2* dst = reinterpret_cast<float2*>(sm_o + (warp * G + hd) * D + g8 * (D / 8));
+#pragma unroll
+        for (int u = 0; u < MMAS; ++u)
+          dst[u] = make_float2(o[n][u][e] * a.v_descale, o[n][u][2 + e] * a.v_descale);
+        if (g8 == 0) {
+          sm_m[warp * G + hd] = mx[n][e];
+          sm_l[warp * G + hd] = l[n][e];
+        }
+      }
+    }
+  __syncthreads();
+
+  const int64_t orow0 = (static_cast<int64_t>(p) * a.num_tokens + t) * a.num_q_heads + h * G;
+  const int64_t slot = (static_cast<int64_t>(t) * P + p) * a.num_kv_heads + h;
+  const bool single = (nchunks == 1);
+  constexpr int CAP = static_cast<int>(SM::RING / 4);
+  for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
+    const int g = idx / D;
+    const int d = idx - g * D;
+    float out, lse;
+    merge_stored<D, G>(sm, NW, g, d, out, lse);
+    if (single) {
+      a.o_part[(orow0 + g) * D + d] = out;
+      if (d == 0) a.lse_part[lse_slot(a, p, t, h * G + g)] = lse;
+    } else {
+      const int64_t wrow = (slot * a.max_chunks + c) * G + g;
+      a.ws_o[wrow * D + d] = out;
+      if (d == 0) a.ws_lse[wrow] = lse;
+    }
+  }
+  if (!single) {
+    if (!take_ticket(a.ws_cnt + slot, nchunks)) return;
+    merge_chunks(a, p, h, t, 1, slot, 0, nchunks, G, D, sm, CAP);
+    if (threadIdx.x == 0) a.ws_cnt[slot] = 0;
+  }
+  if (a.fused) pair_finish(a, t, h, G, D, sm, CAP);
+}
+
+template <int D, int G, bool MOD>
+static int launch_fp4_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  using SM = F4Smem<D>;
+  const size_t comb = (static_cast<size_t>(kF4Warps) * G * D + 2 * kF4Warps * G) * sizeof(float);
+  const size_t pages = (static_cast<size_t>(a.chunk) / a.ps_l + 2) * sizeof(int);
+  const size_t smem = (SM::RING > comb ? SM::RING : comb) + pages;
+  auto kern = gqa_partial_fp4_kernel<D, G, MOD>;
+  static std::atomic<int> smem_set[64];
+  *err = ensure_smem(kern, smem, smem_set);
+  if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
+  dim3 grid(a.max_chunks, a.P * a.num_kv_heads, a.qo_indptr != nullptr ? a.num_rows : a.num_tokens);
+  *err = launch_pdl(kern, grid, dim3(kF4Warps * 32), smem, s, a);
+  return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
+template <int D, bool MOD>
+static int fp4_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
+  switch (G) {
+    case 1: return launch_fp4_t<D, 1, MOD>(a, s, err);
+    case 2: return launch_fp4_t<D, 2, MOD>(a, s, err);
+    case 4: return launch_fp4_t<D, 4, MOD>(a, s, err);
+    case 8: return launch_fp4_t<D, 8, MOD>(a, s, err);
+    case 16: return launch_fp4_t<D, 16, MOD>(a, s, err);
+    default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  }
+}
+
+int launch_gqa_partial_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (a.head_dim == 128) return a.has_mod ? fp4_dispatch_g<128, true>(a, G, s, err) : fp4_dispatch_g<128, false>(a, G, s, err);
+  if (a.head_dim == 64) return a.has_mod ? fp4_dispatch_g<64, true>(a, G, s, err) : fp4_dispatch_g<64, false>(a, G, s, err);
+  return CPATTN_ERR_UNSUPPORTED_SHAPE;
+}
+
+}  // namespace cpattn

@@ -26,6 +26,7 @@
 #include "gqa_core.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
+#include "score_mod.cuh"
 #include "split_combine.cuh"
 
 namespace cpattn {
@@ -54,7 +55,8 @@ __device__ __forceinline__ int swz(int c, int r) {
   else return c ^ ((r >> 1) & (CHR - 1));
 }
 
-template <int D, int G, bool F8>
+// MOD: modified scores (score_mod.cuh).
+template <int D, int G, bool F8, bool MOD>
 __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(const PartialArgs a) {
   using SM = MmaSmem<D, F8>;
   constexpr int NW = kMmaWarps;
@@ -208,7 +210,18 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
 #pragma unroll
   for (int u = 0; u < NT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  const float sl = a.scale * kLog2e * (F8 ? a.k_descale : 1.f);
+  const float sl = a.scale * (MOD ? 1.f : kLog2e) * (F8 ? a.k_descale : 1.f);
+  ScoreMod smod;
+  float slope0 = 0.f, slope1 = 0.f;  // heads quad, quad + 8
+  int qpos = 0;
+  if constexpr (MOD) {
+    smod = score_mod_of(a.softcap);
+    if (a.slopes != nullptr) {
+      qpos = query_pos(a, b, t, t);
+      if (quad < G) slope0 = __ldg(a.slopes + h * G + quad);
+      if (quad + 8 < G) slope1 = __ldg(a.slopes + h * G + quad + 8);
+    }
+  }
   const int mrow = lane & 7;
   const int mi = lane >> 3;  // which of the 4 matrices of an ldmatrix.x4 this lane addresses
 
@@ -266,8 +279,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const bool ok = (vm >> (j * 8 + 2 * qi + e)) & 1u;
-        s[j][e] = ok ? (s[j][e] + s_alt[j][e]) * sl : -INFINITY;
-        s[j][e + 2] = ok ? (s[j][e + 2] + s_alt[j][e + 2]) * sl : -INFINITY;
+        float x0 = (s[j][e] + s_alt[j][e]) * sl, x1 = (s[j][e + 2] + s_alt[j][e + 2]) * sl;
+        if constexpr (MOD) {
+          const int k = k_begin + (warp + i * NW) * KT + j * 8 + 2 * qi + e;
+          const float away = static_cast<float>(stripe_pos(k, p, P, a.interleave) - qpos);
+          x0 = mod_score(smod, x0, slope0, away);
+          x1 = mod_score(smod, x1, slope1, away);
+        }
+        s[j][e] = ok ? x0 : -INFINITY;
+        s[j][e + 2] = ok ? x1 : -INFINITY;
         bm0 = fmaxf(bm0, s[j][e]);
         bm1 = fmaxf(bm1, s[j][e + 2]);
       }
@@ -295,10 +315,12 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
     }
     uint32_t pa[4], pl[4];
     {
-      const float p00 = exp2f(s[0][0] - m0), p01 = exp2f(s[0][1] - m0);
-      const float p02 = exp2f(s[0][2] - m1), p03 = exp2f(s[0][3] - m1);
-      const float p10 = exp2f(s[1][0] - m0), p11 = exp2f(s[1][1] - m0);
-      const float p12 = exp2f(s[1][2] - m1), p13 = exp2f(s[1][3] - m1);
+      // while a row has met no key (its first pages rejected) its max is -inf: 0 stands in, every p is 0
+      const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
+      const float p00 = exp2f(s[0][0] - n0), p01 = exp2f(s[0][1] - n0);
+      const float p02 = exp2f(s[0][2] - n1), p03 = exp2f(s[0][3] - n1);
+      const float p10 = exp2f(s[1][0] - n0), p11 = exp2f(s[1][1] - n0);
+      const float p12 = exp2f(s[1][2] - n1), p13 = exp2f(s[1][3] - n1);
       l0 += (p00 + p01) + (p10 + p11);
       l1 += (p02 + p03) + (p12 + p13);
       split16<F8>(p00, p01, pa[0], pl[0]);
@@ -428,13 +450,13 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
   if (a.fused) pair_finish(a, t, h, G, D, sm, static_cast<int>(SM::MAIN / 4));
 }
 
-template <int D, int G, bool F8>
+template <int D, int G, bool F8, bool MOD>
 static int launch_mma_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   using SM = MmaSmem<D, F8>;
   const size_t comb = (static_cast<size_t>(kMmaWarps) * G * D + 2 * kMmaWarps * G) * sizeof(float);
   const size_t pages = (static_cast<size_t>(a.chunk) / a.ps_l + 2) * sizeof(int);
   const size_t smem = (SM::MAIN > comb ? SM::MAIN : comb) + pages;
-  auto kern = gqa_partial_mma_kernel<D, G, F8>;
+  auto kern = gqa_partial_mma_kernel<D, G, F8, MOD>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
@@ -444,37 +466,24 @@ static int launch_mma_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) 
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <int D, bool F8>
-static int mma_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
-  switch (G) {
-    case 1: return launch_mma_t<D, 1, F8>(a, s, err);
-    case 2: return launch_mma_t<D, 2, F8>(a, s, err);
-    case 4: return launch_mma_t<D, 4, F8>(a, s, err);
-    case 8: return launch_mma_t<D, 8, F8>(a, s, err);
-    case 16: return launch_mma_t<D, 16, F8>(a, s, err);
-    default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  }
+// Groups of 16 heads (smaller ones: partial_gqa_mmat.cu).
+template <bool F8, bool MOD>
+static int launch_mma_g16(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  if (a.head_dim == 128) return launch_mma_t<128, 16, F8, MOD>(a, s, err);
+  if (a.head_dim == 64) return launch_mma_t<64, 16, F8, MOD>(a, s, err);
+  return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }
 
 int launch_gqa_partial_mma(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (a.head_dim != a.head_dim_v) return CPATTN_ERR_UNSUPPORTED_SHAPE;
   int st = CPATTN_ERR_UNSUPPORTED_SHAPE;
-  // groups of up to 8 heads: the transposed kernel (partial_gqa_mmat.cu);
-  // groups of 16: the head-rows kernel above
-  if (a.kv_fp8) {
-    if (G <= 8) {
-      st = launch_gqa_partial_mmat(a, s, err);
-    } else {
-      if (a.head_dim == 128) st = mma_dispatch_g<128, true>(a, G, s, err);
-      if (a.head_dim == 64) st = mma_dispatch_g<64, true>(a, G, s, err);
-    }
-  } else if (G <= 8) {
-    st = launch_gqa_partial_mmat(a, s, err);
-  } else {
-    if (a.head_dim == 128) st = mma_dispatch_g<128, false>(a, G, s, err);
-    if (a.head_dim == 64) st = mma_dispatch_g<64, false>(a, G, s, err);
-  }
+  // E2M1 pools: the kernel of partial_gqa_fp4.cu; groups of up to 8 heads: the
+  // transposed kernel (partial_gqa_mmat.cu); groups of 16: the head-rows kernel above
+  if (a.kv_fp4) st = launch_gqa_partial_fp4(a, s, err);
+  else if (G <= 8) st = launch_gqa_partial_mmat(a, s, err);
+  else if (G == 16 && a.has_mod) st = a.kv_fp8 ? launch_mma_g16<true, true>(a, s, err) : launch_mma_g16<false, true>(a, s, err);
+  else if (G == 16) st = a.kv_fp8 ? launch_mma_g16<true, false>(a, s, err) : launch_mma_g16<false, false>(a, s, err);
   // ragged rows may hold several tokens: those rows go to the multi-token kernel
   if (st == CPATTN_OK && a.qo_indptr != nullptr) st = launch_gqa_partial_ext(a, s, err);
   return st;

@@ -26,6 +26,7 @@
 #include "gqa_core.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
+#include "score_mod.cuh"
 #include "split_combine.cuh"
 
 namespace cpattn {
@@ -61,7 +62,8 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   return y;
 }
 
-template <int D, int G, bool F8>
+// MOD: modified scores (score_mod.cuh).
+template <int D, int G, bool F8, bool MOD>
 __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_kernel(const PartialArgs a) {
   using SM = TSmem<D, F8>;
   constexpr int NW = kTWarps;
@@ -196,7 +198,18 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
 #pragma unroll
   for (int u = 0; u < MT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 qi, 2 qi + 1
-  const float sl = a.scale * kLog2e * (F8 ? a.k_descale : 1.f);
+  const float sl = a.scale * (MOD ? 1.f : kLog2e) * (F8 ? a.k_descale : 1.f);
+  ScoreMod smod;
+  float slope0 = 0.f, slope1 = 0.f;  // heads 2 qi, 2 qi + 1
+  int qpos = 0;
+  if constexpr (MOD) {
+    smod = score_mod_of(a.softcap);
+    if (a.slopes != nullptr) {
+      qpos = query_pos(a, b, t, t);
+      if (2 * qi < G) slope0 = __ldg(a.slopes + h * G + 2 * qi);
+      if (2 * qi + 1 < G) slope1 = __ldg(a.slopes + h * G + 2 * qi + 1);
+    }
+  }
   const int mrow = lane & 7;
   const int mi = lane >> 3;
 
@@ -244,10 +257,20 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
     const bool ka = (vm >> g8) & 1u;        // key g8
     const bool kb = (vm >> (g8 + 8)) & 1u;  // key g8 + 8
     float v[4];
-    v[0] = ka ? (st[0] + st2[0]) * sl : -INFINITY;  // key g8,     head 2 qi
-    v[1] = ka ? (st[1] + st2[1]) * sl : -INFINITY;  // key g8,     head 2 qi + 1
-    v[2] = kb ? (st[2] + st2[2]) * sl : -INFINITY;  // key g8 + 8, head 2 qi
-    v[3] = kb ? (st[3] + st2[3]) * sl : -INFINITY;  // key g8 + 8, head 2 qi + 1
+    if constexpr (MOD) {
+      const int k0 = k_begin + (warp + i * NW) * KT + g8;
+      const float da = static_cast<float>(stripe_pos(k0, p, P, a.interleave) - qpos);
+      const float db = static_cast<float>(stripe_pos(k0 + 8, p, P, a.interleave) - qpos);
+      v[0] = ka ? mod_score(smod, (st[0] + st2[0]) * sl, slope0, da) : -INFINITY;
+      v[1] = ka ? mod_score(smod, (st[1] + st2[1]) * sl, slope1, da) : -INFINITY;
+      v[2] = kb ? mod_score(smod, (st[2] + st2[2]) * sl, slope0, db) : -INFINITY;
+      v[3] = kb ? mod_score(smod, (st[3] + st2[3]) * sl, slope1, db) : -INFINITY;
+    } else {
+      v[0] = ka ? (st[0] + st2[0]) * sl : -INFINITY;  // key g8,     head 2 qi
+      v[1] = ka ? (st[1] + st2[1]) * sl : -INFINITY;  // key g8,     head 2 qi + 1
+      v[2] = kb ? (st[2] + st2[2]) * sl : -INFINITY;  // key g8 + 8, head 2 qi
+      v[3] = kb ? (st[3] + st2[3]) * sl : -INFINITY;  // key g8 + 8, head 2 qi + 1
+    }
     float bm0 = fmaxf(v[0], v[2]), bm1 = fmaxf(v[1], v[3]);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -396,13 +419,13 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
   if (a.fused) pair_finish(a, t, h, G, D, sm, static_cast<int>(SM::MAIN / 4));
 }
 
-template <int D, int G, bool F8>
+template <int D, int G, bool F8, bool MOD>
 static int launch_mmat_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   using SM = TSmem<D, F8>;
   const size_t comb = (static_cast<size_t>(kTWarps) * G * D + 2 * kTWarps * G) * sizeof(float);
   const size_t pages = (static_cast<size_t>(a.chunk) / a.ps_l + 2) * sizeof(int);
   const size_t smem = (SM::MAIN > comb ? SM::MAIN : comb) + pages;
-  auto kern = gqa_partial_mmat_kernel<D, G, F8>;
+  auto kern = gqa_partial_mmat_kernel<D, G, F8, MOD>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
@@ -411,28 +434,29 @@ static int launch_mmat_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err)
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool MOD>
 static int mmat_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
   switch (G) {
-    case 1: return launch_mmat_t<D, 1, F8>(a, s, err);
-    case 2: return launch_mmat_t<D, 2, F8>(a, s, err);
-    case 4: return launch_mmat_t<D, 4, F8>(a, s, err);
-    case 8: return launch_mmat_t<D, 8, F8>(a, s, err);
+    case 1: return launch_mmat_t<D, 1, F8, MOD>(a, s, err);
+    case 2: return launch_mmat_t<D, 2, F8, MOD>(a, s, err);
+    case 4: return launch_mmat_t<D, 4, F8, MOD>(a, s, err);
+    case 8: return launch_mmat_t<D, 8, F8, MOD>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
+}
+
+template <bool F8, bool MOD>
+static int mmat_dispatch_d(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
+  if (a.head_dim == 128) return mmat_dispatch_g<128, F8, MOD>(a, G, s, err);
+  if (a.head_dim == 64) return mmat_dispatch_g<64, F8, MOD>(a, G, s, err);
+  return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }
 
 // Rows of one token, group size <= 8: the transposed kernel.
 int launch_gqa_partial_mmat(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   const int G = a.num_q_heads / a.num_kv_heads;
-  if (a.kv_fp8) {
-    if (a.head_dim == 128) return mmat_dispatch_g<128, true>(a, G, s, err);
-    if (a.head_dim == 64) return mmat_dispatch_g<64, true>(a, G, s, err);
-  } else {
-    if (a.head_dim == 128) return mmat_dispatch_g<128, false>(a, G, s, err);
-    if (a.head_dim == 64) return mmat_dispatch_g<64, false>(a, G, s, err);
-  }
-  return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  if (a.has_mod) return a.kv_fp8 ? mmat_dispatch_d<true, true>(a, G, s, err) : mmat_dispatch_d<false, true>(a, G, s, err);
+  return a.kv_fp8 ? mmat_dispatch_d<true, false>(a, G, s, err) : mmat_dispatch_d<false, false>(a, G, s, err);
 }
 
 }  // namespace cpattn

@@ -1,6 +1,7 @@
 """One attention step over a striped pool, orchestrated through the C ABI.
 
-A decode step (one new token a row) is: ``cp_kv_write`` of the new K/V, then
+A decode step (one new token a row) is: ``cp_kv_write`` of the new K/V
+(``cp_rope_kv_write`` for a layer that rotates its queries and keys), then
 ``cp_paged_attn_partial`` over each row's full length, then ``lse_merge`` of
 the P partner partials.  A non-decode step attends the pool for the context
 only and its new tokens apart: ``cp_kv_write``, ``cp_paged_attn_partial``
@@ -28,12 +29,19 @@ def _to_torch(a: np.ndarray, device) -> torch.Tensor:
 
 
 def desc_for(w) -> B.PoolDesc:
-    fp8 = getattr(w, "kv_dtype", "same") == "fp8"
+    kv = {"fp8": B.DTYPE_FP8_E4M3, "fp4": B.DTYPE_FP4_E2M1}.get(getattr(w, "kv_dtype", "same"), 0)
     return B.PoolDesc(P=w.P, page_size=w.page_size, num_pages=w.num_pages, num_kv_heads=w.num_kv_heads,
                       head_dim=w.head_dim, head_dim_v=w.head_dim_v,
                       dtype=B.DTYPE_BF16 if w.dtype == "bf16" else B.DTYPE_FP32,
-                      interleave=w.interleave, kv_dtype=B.DTYPE_FP8_E4M3 if fp8 else 0,
-                      k_descale=w.k_descale if fp8 else 0.0, v_descale=w.v_descale if fp8 else 0.0)
+                      interleave=w.interleave, kv_dtype=kv,
+                      k_descale=w.k_descale if kv else 0.0, v_descale=w.v_descale if kv else 0.0)
+
+
+def rope_table(length, rot_dim, base=10000.0):
+    """``[length, rot_dim]`` float32 for ``cp_rope_kv_write``: the cosines of
+    ``position * base^(-2 i / rot_dim)`` (angles in float64), then the sines."""
+    ang = np.arange(length, dtype=np.float64)[:, None] * base ** (-np.arange(0, rot_dim, 2) / rot_dim)[None, :]
+    return np.concatenate([np.cos(ang), np.sin(ang)], axis=1).astype(np.float32)
 
 
 def pack_tensors(tensors, device, align=256):
@@ -68,7 +76,8 @@ class StripedAttention:
         self.desc = desc_for(w)
         dt = self.desc.torch_dtype()
         pdt = self.desc.pool_torch_dtype()
-        nan = B.FP8_NAN_CODE if self.desc.fp8 else float("nan")
+        # every byte the E4M3 NaN code: E2M1 rows then read NaN through their scales
+        nan = B.FP8_NAN_CODE if self.desc.fp8 or self.desc.fp4 else float("nan")
         self.pool_k = torch.full(self.desc.pool_shape(False), nan, dtype=pdt, device=self.device)
         self.pool_v = None if w.mla else torch.full(self.desc.pool_shape(True), nan, dtype=pdt, device=self.device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -103,6 +112,15 @@ class StripedAttention:
         # copy out a step (``packed_inputs`` / ``packed_outputs``)
         self.packed_inputs = self._pack(self.INPUTS)
         self.packed_outputs = self._pack(("out", "lse"))
+        if w.rot_dim:
+            length = max(1, int((w.ctx_len + w.new_len).max(initial=0)))
+            self.cos_sin = _to_torch(rope_table(length, w.rot_dim, w.rope_base), self.device)
+            self.rope_style = B.ROPE_PAIRS if w.rope_pairs else B.ROPE_HALVES
+            self.q_rot, self.k_rot = torch.zeros_like(self.q), torch.zeros_like(self.k_new)
+        self.mod = None
+        if w.softcap or w.slopes is not None:
+            self.mod = B.score_mod(w.softcap, None if w.slopes is None else _to_torch(w.slopes, self.device),
+                                   self.positions)
         if fill_history:
             self.fill_history()
 
@@ -125,12 +143,28 @@ class StripedAttention:
         qo, pos, k, v = history_tokens(self.w)
         if len(pos) == 0:
             return
-        B.cp_kv_write(self.desc, self.pool_k, self.pool_v, _to_torch(k, self.device),
-                      None if v is None else _to_torch(v, self.device), _to_torch(pos, self.device),
-                      _to_torch(qo, self.device), self.page_indptr, self.page_indices, dev_status=self.dev_status)
+        k, v, pos, qo = (None if x is None else _to_torch(x, self.device) for x in (k, v, pos, qo))
+        if self.w.rot_dim:
+            B.cp_rope_kv_write(self.desc, self.pool_k, self.pool_v, None, k, v, pos, qo, self.page_indptr,
+                               self.page_indices, self.cos_sin, None, rot_begin=self.w.rot_begin,
+                               style=self.rope_style, dev_status=self.dev_status)
+            return
+        B.cp_kv_write(self.desc, self.pool_k, self.pool_v, k, v, pos, qo, self.page_indptr, self.page_indices,
+                      dev_status=self.dev_status)
 
     # -- the step's calls
+    @property
+    def query(self):
+        """Queries the attention calls take: rotated ones where the layer rotates."""
+        return self.q_rot if self.w.rot_dim else self.q
+
     def write_new(self, stream=None):
+        if self.w.rot_dim:
+            B.cp_rope_kv_write(self.desc, self.pool_k, self.pool_v, self.q, self.k_new, self.v_new, self.positions,
+                               self.qo_indptr, self.page_indptr, self.page_indices, self.cos_sin, self.q_rot,
+                               self.k_rot, rot_begin=self.w.rot_begin, style=self.rope_style,
+                               dev_status=self.dev_status, stream=stream)
+            return
         B.cp_kv_write(self.desc, self.pool_k, self.pool_v, self.k_new, self.v_new, self.positions, self.qo_indptr,
                       self.page_indptr, self.page_indices, dev_status=self.dev_status, stream=stream)
 
@@ -138,17 +172,18 @@ class StripedAttention:
         P = self.w.P
         # one token a row (a decode step): the call takes no token -> row map
         one_per_row = self.w.decode and self.w.num_tokens == self.w.num_rows
-        B.cp_paged_attn_partial_ex(self.desc, self.pool_k, self.pool_v, self.q, self.kv_len, self.max_kv_len,
+        B.cp_paged_attn_partial_ex(self.desc, self.pool_k, self.pool_v, self.query, self.kv_len, self.max_kv_len,
                                    self.page_indptr, self.page_indices, self.w.scale, self.o_parts[:P],
                                    self.lse_parts[:P], self.workspace,
                                    qo_indptr=None if one_per_row else self.qo_indptr,
                                    num_rows=self.w.num_rows, row_order=self.row_order if one_per_row else None,
-                                   dev_status=self.dev_status, stream=stream)
+                                   dev_status=self.dev_status, stream=stream, mod=self.mod)
 
     def own(self, stream=None):
         P = self.w.P
-        B.own_token_attn(self.q, self.k_new, self.v_new, self.qo_indptr, self.w.num_real_rows, self.max_q_len,
-                         self.w.scale, self.o_parts[P], self.lse_parts[P], stream=stream)
+        B.own_token_attn(self.query, self.k_rot if self.w.rot_dim else self.k_new, self.v_new, self.qo_indptr,
+                         self.w.num_real_rows, self.max_q_len, self.w.scale, self.o_parts[P], self.lse_parts[P],
+                         stream=stream, mod=self.mod)
 
     def merge(self, stream=None):
         B.lse_merge(self.o_parts, self.lse_parts, self.out, self.lse, stream=stream)
@@ -173,13 +208,13 @@ class StripedAttention:
         one_per_row = self.w.decode and self.w.num_tokens == self.w.num_rows
         extra_o = None if self.w.decode else self.o_parts[P]
         extra_lse = None if self.w.decode else self.lse_parts[P]
-        B.cp_paged_attn_fused(self.desc, self.pool_k, self.pool_v, self.q, self.kv_len, self.max_kv_len,
+        B.cp_paged_attn_fused(self.desc, self.pool_k, self.pool_v, self.query, self.kv_len, self.max_kv_len,
                               self.page_indptr, self.page_indices, self.w.scale,
                               self.out if out is None else out, self._fused_ws,
                               lse_out=self.lse if lse is None else lse, extra_o=extra_o, extra_lse=extra_lse,
                               qo_indptr=None if one_per_row else self.qo_indptr, num_rows=self.w.num_rows,
                               row_order=self.row_order if one_per_row else None,
-                              dev_status=self.dev_status, stream=stream)
+                              dev_status=self.dev_status, stream=stream, mod=self.mod)
 
     def run_step_fused(self, stream=None, out=None, lse=None):
         self.write_new(stream)
@@ -206,11 +241,11 @@ class StripedAttention:
             self._lse_cor = torch.empty((P, Hl, T), dtype=torch.float32, device=self.device)
         one_per_row = w.decode and w.num_tokens == w.num_rows
         self.write_new(stream)
-        B.cp_paged_attn_partial_ex(self.desc, self.pool_k, self.pool_v, self.q, self.kv_len, self.max_kv_len,
+        B.cp_paged_attn_partial_ex(self.desc, self.pool_k, self.pool_v, self.query, self.kv_len, self.max_kv_len,
                                    self.page_indptr, self.page_indices, w.scale, self.o_parts[:P], self._lse_hm,
                                    self.workspace, lse_layout=B.LSE_HEAD_MAJOR,
                                    qo_indptr=None if one_per_row else self.qo_indptr, num_rows=w.num_rows,
-                                   dev_status=self.dev_status, stream=stream)
+                                   dev_status=self.dev_status, stream=stream, mod=self.mod)
         if not w.decode:
             self.own(stream)
         for r in range(P):

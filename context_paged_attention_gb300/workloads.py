@@ -102,6 +102,16 @@ class Workload:
     kv_dtype: str = "same"  # "fp8": the pool holds E4M3 codes of K / k_descale and V / v_descale
     k_descale: float = 0.0
     v_descale: float = 0.0
+    # "fp4" pools (kv_dtype) hold 4-bit codes with a scale per 16 values, and the same descales.
+    # Rotation on the way into the pool (0: q, k_seq and k_new are taken as they are): rot_dim
+    # values from rot_begin on turn by position * rope_base^(-2 i / rot_dim)
+    rot_dim: int = 0
+    rot_begin: int = 0
+    rope_pairs: bool = False
+    rope_base: float = 10000.0
+    # modified scores: a cap (0: none) and a slope for each query head (None: none)
+    softcap: float = 0.0
+    slopes: np.ndarray | None = None
 
     @property
     def sink_page(self) -> int:
@@ -121,11 +131,11 @@ class Workload:
 
     def kv_bytes_read(self) -> int:
         """Algorithmic K/V bytes the pool partial reads: every visible key once
-        (one byte a value for FP8 pools)."""
-        esz = 1 if self.kv_dtype == "fp8" else (2 if self.dtype == "bf16" else 4)
+        (one byte a value for FP8 pools, 9 bytes for 16 values in 4 bits)."""
+        esz = {"fp8": 1, "fp4": 9 / 16}.get(self.kv_dtype, 2 if self.dtype == "bf16" else 4)
         keys = int(self.kv_len[: self.num_real_rows].astype(np.int64).sum())
         per_key = self.num_kv_heads * (self.head_dim + (0 if self.mla else self.head_dim_v)) * esz
-        return keys * per_key
+        return int(keys * per_key)
 
 
 def interleaved(w: Workload, interleave: int) -> Workload:
@@ -144,6 +154,32 @@ def fp8_pool(w: Workload, k_descale: float, v_descale: float) -> Workload:
         raise ValueError("FP8 pools are for bf16 GQA layers")  # the library refuses the rest
     return dataclasses.replace(w, kv_dtype="fp8", k_descale=float(k_descale), v_descale=float(v_descale),
                                name=f"{w.name}_fp8")
+
+
+def fp4_pool(w: Workload, k_descale: float, v_descale: float) -> Workload:
+    """The same step with the pool kept in 4 bits (E2M1 codes, an E4M3 scale per
+    16 values, per-tensor descales; a bf16 GQA layer only)."""
+    if w.dtype != "bf16" or w.mla:
+        raise ValueError("4-bit pools are for bf16 GQA layers")
+    return dataclasses.replace(w, kv_dtype="fp4", k_descale=float(k_descale), v_descale=float(v_descale),
+                               name=f"{w.name}_fp4")
+
+
+def rotated(w: Workload, rot_dim: int, rot_begin: int = 0, pairs: bool = False, base: float = 10000.0) -> Workload:
+    """The same step of a layer that rotates its queries and keys by their
+    positions when it appends (the inputs are the values before the rotation)."""
+    if rot_dim < 2 or rot_dim % 2 or rot_begin < 0 or rot_begin + rot_dim > w.head_dim:
+        raise ValueError("the rotated values must lie within a head")
+    return dataclasses.replace(w, rot_dim=rot_dim, rot_begin=rot_begin, rope_pairs=pairs, rope_base=float(base),
+                               name=f"{w.name}_rope")
+
+
+def scored(w: Workload, softcap: float = 0.0, slopes=None) -> Workload:
+    """The same step with capped scores and / or a distance slope for each query head."""
+    slopes = None if slopes is None else np.asarray(slopes, dtype=np.float32)
+    if w.mla or (slopes is not None and slopes.shape != (w.num_q_heads,)):
+        raise ValueError("a GQA layer with one slope a query head")
+    return dataclasses.replace(w, softcap=float(softcap), slopes=slopes, name=f"{w.name}_scored")
 
 
 def _values(rng, shape, dtype):
@@ -304,6 +340,12 @@ def mixed_step(seed=5, n_decode=48, n_extend=16, dec_ctx=(1024, 16384), ext_new=
                           num_kv_heads=8, head_dim=128, decode=False, ctx_len=ctx, new_len=new,
                           padding_spans=padding_spans,
                           num_tokens=_round_up(max(T, 1), token_multiple), rng=rng, seed=seed)
+
+
+def gqa_decode_fp4(seed=2, batch=64, len_lo=512, len_hi=8192, padding_spans=None):
+    """The GQA decode step over a 4-bit pool: per-tensor descales about
+    amax / (6 * 448) of the N(0, 1) draws."""
+    return fp4_pool(gqa_decode(seed, batch, len_lo, len_hi, padding_spans), 0.0021, 0.0023)
 
 
 WORKLOADS = {

@@ -45,6 +45,17 @@
  *   (IEEE float32 quotient, round to nearest even, magnitudes past 448
  *   saturated to 448); a read key or value is code value * descale.  Queries,
  *   new K/V and outputs stay bf16; the pool bytes halve.
+ *   A bf16 GQA layer may also keep its pool in 4 bits (CPATTN_DTYPE_FP4_E2M1):
+ *   a row holds one E2M1 code a value (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   bit 3 the sign) and one E4M3 scale per 16 values; a read key or value is
+ *   code value * scale * descale.  On a write the scale is the E4M3 value
+ *   nearest to max |x / descale| / 6 over the 16 values and a code is the E2M1
+ *   value nearest to (x / descale) / scale (IEEE float32 quotients, ties to the
+ *   even code, magnitudes past 6 at 6); a block whose scale rounds to 0 is
+ *   stored as zeros, and one that holds a NaN reads as NaN.  At head_dim 128
+ *   a row takes 72 bytes (bf16: 256).  head_dim must be a multiple of 32.
+ *   Queries over E4M3 and E2M1 pools are multiplied as float16 (exact for
+ *   magnitudes in [2^-14, 65504]) in rows of one token, as bf16 otherwise.
  *   Partial outputs and log-sum-exps are always fp32.  Log-sum-exps use the
  *   natural logarithm; an empty key set gives output 0 and LSE -inf.
  *
@@ -62,6 +73,10 @@
  * page_size.  I = 1 is the plain striping.  MLA pools keep one
  * latent row per token (num_kv_heads = 1, head_dim = 576) and no pool_v: the
  * value is the first head_dim_v values of the latent row (pool_v == NULL).
+ * E2M1 pools are one buffer a tensor: the codes of every row in the order
+ * above, [...][head_dim / 2] bytes, value 2 i of a row in the low half of byte
+ * i; behind them the scales of every row in the same order,
+ * [...][head_dim / 16] bytes (cpattn_pool_bytes counts both).
  */
 #ifndef CPATTN_H_
 #define CPATTN_H_
@@ -99,11 +114,13 @@ extern "C" {
 #define CPATTN_DEV_POS_PAST_TABLE 2      /* position beyond the row's page table */
 #define CPATTN_DEV_BAD_INDPTR 3          /* qo_indptr not within [0, num_tokens] */
 #define CPATTN_DEV_TC_TIMEOUT 4          /* a tensor-core completion wait ran out; that CTA's output is not written */
+#define CPATTN_DEV_POS_PAST_ROPE 5       /* position beyond the rotation table (cp_rope_kv_write) */
 
 /* element types */
 #define CPATTN_DTYPE_BF16 0
 #define CPATTN_DTYPE_FP32 1
 #define CPATTN_DTYPE_FP8_E4M3 2 /* pools only (kv_dtype), with a bf16 layer */
+#define CPATTN_DTYPE_FP4_E2M1 3 /* pools only (kv_dtype), with a bf16 GQA layer */
 
 typedef struct cpattn_pool_desc {
   int32_t P;            /* partners (stripes); divides page_size */
@@ -115,9 +132,9 @@ typedef struct cpattn_pool_desc {
   int32_t dtype;        /* CPATTN_DTYPE_* of pool, q and new K/V */
   int32_t interleave;   /* interleave size I (0 or 1: plain striping); I * P divides page_size */
   int32_t kv_dtype;     /* element type of pool_k / pool_v: 0 or dtype (the same), or
-                           CPATTN_DTYPE_FP8_E4M3 with dtype CPATTN_DTYPE_BF16 */
-  float k_descale;      /* FP8 pools: key = code value * k_descale (finite, > 0) */
-  float v_descale;      /* FP8 pools: value = code value * v_descale (finite, > 0) */
+                           CPATTN_DTYPE_FP8_E4M3 / _FP4_E2M1 with dtype CPATTN_DTYPE_BF16 */
+  float k_descale;      /* FP8 and FP4 pools: key = code value (* scale) * k_descale (finite, > 0) */
+  float v_descale;      /* FP8 and FP4 pools: value = code value (* scale) * v_descale (finite, > 0) */
 } cpattn_pool_desc;
 
 /* Library version (CPATTN_VERSION) -- lets a binding check it loaded the right .so. */
@@ -158,6 +175,48 @@ CPATTN_API int cp_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* poo
                 const int32_t* qo_indptr, int32_t num_rows, int32_t num_tokens,
                 const int32_t* kv_page_indptr, const int32_t* kv_page_indices,
                 int32_t* dev_status, cudaStream_t stream);
+
+/* pairing of the rotated values (cp_rope_kv_write) */
+#define CPATTN_ROPE_HALVES 0 /* value i with value i + rot_dim / 2 */
+#define CPATTN_ROPE_PAIRS 1  /* value 2 i with value 2 i + 1 */
+
+/*
+ * cp_rope_kv_write -- rotate a step's queries and new keys by their positions
+ * and write the new K/V into the striped pool, in one launch (cp_kv_write with
+ * the rotary embedding on the way; the source pages leave the rotation to the
+ * model, which would read and write q and k once more for it).
+ *
+ * A pair (u, v) of the rot_dim values from rot_begin on, of a token at
+ * position n, becomes (u c - v s, v c + u s), c and s being entry i of the
+ * table's row n (pair i: values i and i + rot_dim / 2, or 2 i and 2 i + 1);
+ * other values pass through.  The arithmetic is float32 with each product and
+ * sum rounded, rounded once more to each output: the layer's dtype for q_out
+ * and k_out, the pool's type for the pool (E4M3 and E2M1 codes are those of the
+ * float32 values).  Values are written as by cp_kv_write.  For MLA rows the
+ * rotated values are usually the last 64 (rot_begin 512).
+ *
+ *   q, q_out   [num_tokens][num_q_heads][head_dim]; both NULL: keys only
+ *   k_out      [num_tokens][num_kv_heads][head_dim] or NULL (a step that attends
+ *              its new tokens apart needs the rotated keys)
+ *              q_out may be q and k_out may be k_new (in place); they may not
+ *              overlap otherwise
+ *   cos_sin    [table_len][rot_dim] fp32: rot_dim / 2 cosines, then the sines
+ *   style      CPATTN_ROPE_HALVES or CPATTN_ROPE_PAIRS
+ *   rot_dim    even, >= 2; rot_begin + rot_dim <= head_dim (<= 2048)
+ *   other arguments as for cp_kv_write
+ * Padding tokens (positions[t] < 0, or at or past qo_indptr[num_rows]) are not
+ * read and their rows of q_out and k_out stay as they are.  A token at a
+ * position past the table is skipped whole and reported
+ * (CPATTN_DEV_POS_PAST_ROPE); one whose page is rejected gets its q_out and
+ * k_out rows but no pool rows.
+ */
+CPATTN_API int cp_rope_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, const void* q,
+                                const void* k_new, const void* v_new, int32_t num_q_heads,
+                                const int32_t* positions, const int32_t* qo_indptr, int32_t num_rows,
+                                int32_t num_tokens, const int32_t* kv_page_indptr,
+                                const int32_t* kv_page_indices, const float* cos_sin, int32_t table_len,
+                                int32_t rot_begin, int32_t rot_dim, int32_t style, void* q_out, void* k_out,
+                                int32_t* dev_status, cudaStream_t stream);
 
 /*
  * cp_paged_attn_partial -- every partner's partial attention over the pool.
@@ -230,6 +289,41 @@ CPATTN_API int cp_paged_attn_partial_ex(const cpattn_pool_desc* desc, const void
                                         int32_t* dev_status, cudaStream_t stream);
 
 /*
+ * Modified scores.  A HOST structure read during the call; NULL, or softcap 0
+ * with slopes NULL, leaves the scores as they are.  For query token t, head h
+ * and the key at position j:
+ *   s = scale * q[t][h] . K_j
+ *   s = softcap * tanh(s / softcap)            if softcap > 0
+ *   s = s + slopes[h] * (j - pos[t])           if slopes is not NULL
+ * (the distance term is not capped; j - pos[t] <= 0 for keys the token sees, so
+ * a positive slope lowers far keys).  Log-sum-exps are those of the modified
+ * scores, so partials merge as usual.
+ *   softcap    0, or within [1e-6, 1e30] (else CPATTN_ERR_INVALID_ARG)
+ *   slopes     device [num_q_heads] fp32, or NULL
+ *   positions  device [num_tokens] int32, the position pos[t] of each query
+ *              token, read only with slopes; NULL: kv_len[b] - 1 when qo_indptr
+ *              is NULL (a decode row's own key is its last), else kv_len[b] + i
+ *              for the i-th token of row b (its context, then its new tokens).
+ *              Not used by own_token_attn_mod, whose distances lie within a row.
+ * GQA shapes of every pool type; MLA returns CPATTN_ERR_UNSUPPORTED_SHAPE.
+ */
+typedef struct cpattn_score_mod {
+  float softcap;
+  const float* slopes;
+  const int32_t* positions;
+} cpattn_score_mod;
+
+/* cp_paged_attn_partial_ex with modified scores (mod may be NULL). */
+CPATTN_API int cp_paged_attn_partial_mod(const cpattn_pool_desc* desc, const void* pool_k,
+                                         const void* pool_v, const void* q, int32_t num_q_heads,
+                                         int32_t num_rows, int32_t num_tokens, const int32_t* qo_indptr,
+                                         const int32_t* kv_len, int32_t max_kv_len,
+                                         const int32_t* kv_page_indptr, const int32_t* kv_page_indices,
+                                         float scale, float* o_part, float* lse_part, int32_t lse_layout,
+                                         const int32_t* row_order, const cpattn_score_mod* mod, void* workspace,
+                                         size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
  * cp_paged_attn_fused -- the partials of all P partners and their exact merge
  * in one call: the final attention output of every query token.
  *
@@ -281,6 +375,18 @@ CPATTN_API int cp_paged_attn_fused(const cpattn_pool_desc* desc, const void* poo
                                    const float* extra_lse,
                                    int32_t out_dtype, void* out, float* lse_out, void* workspace,
                                    size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/* cp_paged_attn_fused with modified scores (mod may be NULL; an extra partial
+ * has to come from modified scores too: own_token_attn_mod). */
+CPATTN_API int cp_paged_attn_fused_mod(const cpattn_pool_desc* desc, const void* pool_k,
+                                       const void* pool_v, const void* q, int32_t num_q_heads,
+                                       int32_t num_rows, int32_t num_tokens, const int32_t* qo_indptr,
+                                       const int32_t* kv_len, int32_t max_kv_len,
+                                       const int32_t* kv_page_indptr, const int32_t* kv_page_indices,
+                                       const int32_t* row_order, float scale, const float* extra_o,
+                                       const float* extra_lse, int32_t out_dtype, void* out, float* lse_out,
+                                       const cpattn_score_mod* mod, void* workspace, size_t workspace_bytes,
+                                       int32_t* dev_status, cudaStream_t stream);
 
 /* Workspace bytes cp_paged_attn_fused needs for these sizes (0 on bad args). */
 CPATTN_API size_t cp_paged_attn_fused_workspace_bytes(const cpattn_pool_desc* desc, int32_t num_q_heads,
@@ -358,6 +464,15 @@ CPATTN_API int own_token_attn(const void* q, const void* k_new, const void* v_ne
                    const int32_t* qo_indptr, int32_t num_rows_bucket, int32_t num_real_rows,
                    int32_t num_tokens, int32_t max_q_len, float scale, float* o_own,
                    float* lse_own, cudaStream_t stream);
+
+/* own_token_attn with modified scores (mod may be NULL; distances are those
+ * within the row, mod->positions is not read). */
+CPATTN_API int own_token_attn_mod(const void* q, const void* k_new, const void* v_new, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t head_dim_v, int32_t dtype,
+                                  const int32_t* qo_indptr, int32_t num_rows_bucket, int32_t num_real_rows,
+                                  int32_t num_tokens, int32_t max_q_len, float scale,
+                                  const cpattn_score_mod* mod, float* o_own, float* lse_own,
+                                  cudaStream_t stream);
 
 /*
  * lse_merge -- exact merge of N partials over disjoint key sets (mstar PR #1124

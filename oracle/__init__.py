@@ -21,12 +21,23 @@ Every function follows a passage of the source pages:
   interleave size ``cp_kv_cache_interleave_size`` (FlashAttentionMetadataBuilder).
 
 Pinning status (what each function is checked against, in
-``tests/test_oracle_pins.py``): every public function has at least one pin
+``tests/test_oracle_pins.py`` and, for ``layer_ops``, ``tests/test_layer_ops_host.py``): every public function has at least one pin
 that does not go through the function itself (brute force, closed forms, a
 library routine, hand-derived golden fixtures, bijection/invariant checks).
 No function here is "parity unpinned".
 """
 
+from .layer_ops import (  # noqa: F401
+    ROPE_HALVES,
+    ROPE_PAIRS,
+    e2m1_encode,
+    e2m1_value,
+    fp4_dequantize,
+    fp4_pack,
+    fp4_quantize,
+    modified_attention,
+    rotate,
+)
 from .reference import (  # noqa: F401
     E4M3_MAX,
     NEG_INF,
