@@ -153,6 +153,11 @@ _SIGNATURES = {
 }
 
 
+_Tensor, _int32 = torch.Tensor, torch.int32
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def library_path() -> str:
     return LIB
 
@@ -184,7 +189,7 @@ def version() -> int:
 def _ptr(t):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError("expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
@@ -194,14 +199,18 @@ def _ptr(t):
 
 
 def _i32_tensor(t, what):
-    if t is not None and t.dtype != torch.int32:
+    if t is None:
+        return None
+    if t.dtype is not _int32:
         raise TypeError(f"{what} must be int32")
     return _ptr(t)
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us a call
+    return _current_raw_stream(_current_device())
 
 
 def _check(status, what):
@@ -233,18 +242,17 @@ def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions,
     T = positions.numel()
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
-    for name, x, heads, d in (("q", q, None, desc.head_dim), ("q_out", q_out, None, desc.head_dim),
-                              ("k_new", k_new, desc.num_kv_heads, desc.head_dim),
-                              ("k_out", k_out, desc.num_kv_heads, desc.head_dim),
-                              ("v_new", v_new, desc.num_kv_heads, desc.head_dim_v)):
+    kv_heads, dtype = desc.num_kv_heads, desc.torch_dtype()
+    shape = (T, kv_heads, desc.head_dim)
+    q_shape = shape if q is None else (T, q.shape[1], desc.head_dim)
+    for name, x, want in (("q", q, q_shape), ("q_out", q_out, q_shape), ("k_new", k_new, shape), ("k_out", k_out, shape),
+                          ("v_new", v_new, (T, kv_heads, desc.head_dim_v))):
         if x is None:
             continue
-        if x.dtype != desc.torch_dtype():
-            raise TypeError(f"{name} must have the layer's dtype {desc.torch_dtype()}")
-        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != d or (heads is not None and x.shape[1] != heads):
-            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {d}]")
-    if q is not None and q_out is not None and q.shape != q_out.shape:
-        raise ValueError("q_out must have q's shape")
+        if x.dtype is not dtype:
+            raise TypeError(f"{name} must have the layer's dtype {dtype}")
+        if x.shape != want:
+            raise ValueError(f"{name} must be {list(want)}")
     st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
                               0 if q is None else q.shape[1], _i32_tensor(positions, "positions"),
                               _i32_tensor(qo_indptr, "qo_indptr"), qo_indptr.numel() - 1, T,

@@ -316,6 +316,8 @@ int cp_rope_kv_write(const cpattn_pool_desc* desc, void* pool_k, void* pool_v, c
   if (style != CPATTN_ROPE_HALVES && style != CPATTN_ROPE_PAIRS) return CPATTN_ERR_INVALID_ARG;
   if (rot_dim < 2 || rot_dim % 2 != 0 || rot_begin < 0 || rot_begin > desc->head_dim - rot_dim)
     return CPATTN_ERR_INVALID_ARG;
+  // rows pass through shared memory as float32, 64 KB a CTA at most
+  if (desc->head_dim > 2048) return CPATTN_ERR_UNSUPPORTED_SHAPE;
   if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && num_q_heads < 1)) return CPATTN_ERR_INVALID_ARG;
   if (num_tokens == 0) return CPATTN_OK;
   const bool mla = is_mla(desc);

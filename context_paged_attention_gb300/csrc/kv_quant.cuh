@@ -38,6 +38,18 @@ __device__ __forceinline__ uint32_t e2m1x2_rn(float lo, float hi) {
   return r;
 }
 
+// Codes of 8 values v (already x / descale) of a block with scale code `scale`
+// (0 where it is 0 or NaN).
+__device__ __forceinline__ uint32_t fp4_codes8(const float* v, uint32_t scale) {
+  if (scale == 0u || scale == 0x7Fu) return 0u;
+  const float s = e4m3_code_value(scale);
+  uint32_t codes = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    codes |= e2m1x2_rn(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s)) << (8 * i);
+  return codes;
+}
+
 // A block of 16 values of an E2M1 row: its scale is the E4M3 value nearest to
 // max |x / descale| / 6, the codes are those of x / descale / scale (IEEE
 // quotients, each rounded once).  A block whose scale rounds to 0 (every
@@ -55,15 +67,7 @@ __device__ __forceinline__ void fp4_encode_block(const float (&x)[16], float des
     amax = fmaxf(amax, fabsf(v[i]));
   }
   scale = nan ? 0x7Fu : e4m3_rn_satfinite(__fdiv_rn(amax, 6.f));
-  codes = make_uint2(0u, 0u);
-  if (scale == 0u || nan) return;
-  const float s = e4m3_code_value(scale);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = e2m1x2_rn(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
-    if (i < 4) codes.x |= b << (8 * i);
-    else codes.y |= b << (8 * (i - 4));
-  }
+  codes = make_uint2(fp4_codes8(v, scale), fp4_codes8(v + 8, scale));
 }
 
 // Row b holding token t, or -1 for a padding token (at or past the last
