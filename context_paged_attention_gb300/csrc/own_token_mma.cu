@@ -132,14 +132,14 @@ __global__ void __launch_bounds__(kOwnMmaWarps * 32) own_token_mma_kernel(const 
 #pragma unroll
     for (int u = 0; u < NT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    const float sl = a.scale * (MOD ? 1.f : kLog2e);
+    const float sl = MOD ? 1.f : a.scale * kLog2e;
     ScoreMod smod;
     float slope0 = 0.f, slope1 = 0.f;
     if constexpr (MOD) {
-      smod = score_mod_of(a.softcap);
+      smod = score_mod_of(a.softcap, a.scale);
       if (a.slopes != nullptr) {
-        slope0 = __ldg(a.slopes + h * G + quad % G);
-        slope1 = __ldg(a.slopes + h * G + (quad + 8) % G);
+        slope0 = __ldg(a.slopes + h * G + quad % G) * kLog2e;
+        slope1 = __ldg(a.slopes + h * G + (quad + 8) % G) * kLog2e;
       }
     }
     const int mrow = lane & 7;

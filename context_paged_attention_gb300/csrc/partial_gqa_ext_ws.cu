@@ -39,14 +39,12 @@
 // CTAs of chunk 0 also write the padding tokens' 0 / -inf.  Every wait is
 // bounded; one that runs out raises the CTA's abort flag, which ends every
 // other wait, and the call reports CPATTN_DEV_TC_TIMEOUT.
-#pragma once
-
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
-#include "score_mod.cuh"
 #include "split_combine.cuh"
 #include "tc05.cuh"
+#include "ws_pipe.cuh"
 
 namespace cpattn {
 
@@ -95,43 +93,14 @@ struct WsLayout {
   static constexpr size_t OFF_MISC = OFF_MASK + kMaskSlots * 4;  // TMEM base, abort flag
   static constexpr int SCRATCH_FLOATS = static_cast<int>((OFF_BAR - OFF_K) / 4);  // K + V rings, free after the loop
   static constexpr int MERGE_BYTES = static_cast<int>(OFF_BAR);  // Q and the rings: contiguous, free after the loop
-  static constexpr size_t OFF_POS = OFF_MISC + 16;  // positions of the keys of the tiles in flight (modified scores)
-  static constexpr size_t OFF_PG = OFF_POS + kMaskSlots * kWTile * 4;
+  static constexpr size_t OFF_PG = OFF_MISC + 16;
   static size_t smem_bytes(int page_slots) { return 1024 + OFF_PG + static_cast<size_t>(page_slots) * 4; }
 };
 
-__device__ __forceinline__ void ws_arrive(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
-}
-// each lane arrives once when all of its earlier cp.async copies have landed
-__device__ __forceinline__ void ws_cp_arrive(uint32_t mbar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(mbar) : "memory");
-}
-__device__ __forceinline__ void ws_cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 zero bytes through the same copy path (nothing is read)
-__device__ __forceinline__ void ws_cp16_zero(uint32_t dst, const void* any_gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;\n" ::"r"(dst), "l"(any_gmem) : "memory");
-}
 __device__ __forceinline__ void ws_bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(mbar)
                : "memory");
-}
-// bounded wait on a phase; gives up when the abort flag is raised
-__device__ __forceinline__ bool ws_wait(uint32_t mbar, uint32_t parity, const volatile int* abort_flag) {
-  for (uint32_t it = 0; it < (1u << 22); ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(mbar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((it & 63u) == 63u && *abort_flag) return false;
-  }
-  return false;
 }
 }  // namespace
 
@@ -231,21 +200,16 @@ __device__ bool ws_merge_chunks_bulk(const PartialArgs& a, int p, int h, int s0,
   return true;
 }
 
-// FMT 0: a bf16 pool.  FMT 1: an E4M3 pool.  The copy warps read each key row's codes with 16-byte
+// F8: an E4M3 pool.  The copy warps read each key row's codes with 16-byte
 // loads, convert them exactly (every E4M3 value is a bf16 value) and store the
 // bf16 row into the ring in the MMA layout; the scores take k_descale and the
-// output v_descale.  Queries stay bf16.  FMT 2: an E2M1 pool, likewise: a lane
-// converts 32 codes (two scale blocks) at a time, code times block scale being
-// exact in float16 and in bf16 (at most six significant bits).  MOD: modified
-// scores (score_mod.cuh); the K copy warp publishes the positions of a tile's
-// keys beside its mask.
-template <int D, int G, int FMT, bool MOD>
+// output v_descale.  Queries stay bf16.
+template <int D, int G, bool F8>
 __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const PartialArgs a) {
   using Lt = WsLayout<D>;
   constexpr int QB = kWRows / G;  // tokens per block
   constexpr int CH = D / 8;       // 16-byte chunks of a K or V row
   constexpr int RPI = 32 / CH;    // rows a warp instruction copies
-  constexpr bool F8 = FMT == 1, F4 = FMT == 2;
   static_assert(G >= 1 && G <= 16 && (D == 64 || D == 128), "shape");
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_scan[kWThreads / 32];  // one partial sum a warp
@@ -258,7 +222,6 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
   uint32_t* smask = reinterpret_cast<uint32_t*>(base + Lt::OFF_MASK);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + Lt::OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(base + Lt::OFF_MISC + 4);
-  float* spos = reinterpret_cast<float*>(base + Lt::OFF_POS);
   int* spg = reinterpret_cast<int*>(base + Lt::OFF_PG);
 
   const int c = blockIdx.x;
@@ -438,11 +401,6 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
           // before the tile's copies; its slot is rewritten kMaskSlots tiles
           // later, when the softmax has long read it
           const uint32_t vm = __ballot_sync(0xffffffffu, myrow >= 0);
-          if constexpr (MOD) {
-            spos[(i % kMaskSlots) * kWTile + lane] =
-                static_cast<float>(stripe_pos(k_begin + i * kWTile + lane, p, P, a.interleave));
-            __threadfence_block();
-          }
           if (lane == 0) {
             smask[i % kMaskSlots] = vm;
             __threadfence_block();
@@ -485,45 +443,6 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
             }
           }
           tc05::fence_smem_to_async();  // the tensor core reads what this lane wrote
-          ws_arrive(bar(b_full + st));
-        } else if constexpr (F4) {
-          constexpr int CH4 = D / 32, RPI4 = 32 / CH4;  // 16-byte chunks of 32 codes; rows a warp instruction loads
-          constexpr int NK = kWTile / RPI4;
-          const int ro4 = lane / CH4, c4 = lane - (lane / CH4) * CH4;
-          const int kstep4 = is_k ? 2 * RPI4 : RPI4;
-          uint4 codes[NK];
-          uint32_t scl[NK];
-#pragma unroll
-          for (int u = 0; u < NK; ++u) {
-            const int key = ro4 + (is_k ? khalf * RPI4 : 0) + u * kstep4;
-            const int row = __shfl_sync(0xffffffffu, myrow, key & 31);
-            codes[u] = make_uint4(0u, 0u, 0u, 0u);  // masked key: zero row
-            scl[u] = 0u;
-            if (key < kWTile && row >= 0) {
-              codes[u] = __ldg(reinterpret_cast<const uint4*>(pool + static_cast<int64_t>(row) * (D / 2) + c4 * 16));
-              scl[u] = __ldg(reinterpret_cast<const unsigned short*>(pool + a.scale_off +
-                                                                     static_cast<int64_t>(row) * (D / 16) + c4 * 2));
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < NK; ++u) {
-            const int key = ro4 + (is_k ? khalf * RPI4 : 0) + u * kstep4;
-            if (key >= kWTile) continue;
-            const uint32_t w[4] = {codes[u].x, codes[u].y, codes[u].z, codes[u].w};
-            const uint32_t s2 = e4m3x2_to_f16x2(scl[u]);
-#pragma unroll
-            for (int hh = 0; hh < 4; ++hh) {  // 8 codes: one bf16 chunk of the row
-              const uint32_t sb = __byte_perm(s2, 0u, hh < 2 ? 0x1010u : 0x3232u);
-              const int cb = 4 * c4 + hh;
-              *reinterpret_cast<uint4*>(base + (dst0 - tc05::smem_addr(base)) + (cb >> 3) * Lt::BLK +
-                                        tc05::sw128(key, cb & 7)) =
-                  make_uint4(f16x2_to_bf16x2(mul_f16x2(e2m1x2_to_f16x2<0>(w[hh]), sb)),
-                             f16x2_to_bf16x2(mul_f16x2(e2m1x2_to_f16x2<1>(w[hh]), sb)),
-                             f16x2_to_bf16x2(mul_f16x2(e2m1x2_to_f16x2<2>(w[hh]), sb)),
-                             f16x2_to_bf16x2(mul_f16x2(e2m1x2_to_f16x2<3>(w[hh]), sb)));
-            }
-          }
-          tc05::fence_smem_to_async();
           ws_arrive(bar(b_full + st));
         } else {
           // unrolled: the shuffles and addresses of all the warp's rows are
@@ -593,18 +512,7 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
     } else if (tid < kWRows) {
       // ================= softmax rows =================
       const uint32_t my_lane = tc05::taddr(tbase, warp * 32, 0);
-      // MOD: scores become modified log2-domain scores below, and sl is 1 from there on
-      const float sl_raw = a.scale * (MOD ? 1.f : kLog2e) * (FMT != 0 ? a.k_descale : 1.f);
-      const float sl = MOD ? 1.f : sl_raw;
-      ScoreMod smod;
-      float slope = 0.f, qpos = 0.f;
-      if constexpr (MOD) {
-        smod = score_mod_of(a.softcap);
-        if (a.slopes != nullptr && my_ok) {
-          slope = __ldg(a.slopes + h * G + my_g);
-          qpos = static_cast<float>(query_pos(a, b, my_tok, __ldg(a.qo_indptr + b)));
-        }
-      }
+      const float sl = a.scale * kLog2e * (F8 ? a.k_descale : 1.f);
       float m = -INFINITY, l = 0.f, lr = 0.f;  // running max (log2), fp32 sum, sum of bf16-rounded p
       for (int i = 0; i < ntiles; ++i) {
         const int bb = i & 1;
@@ -628,17 +536,6 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
         tc05::fence_before_sync();
         __syncwarp();
         if (lane == 0) ws_arrive(bar(W_SFREE + bb));
-        if constexpr (MOD) {
-          const float4* kp = reinterpret_cast<const float4*>(spos + (i % kMaskSlots) * kWTile);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 k4 = kp[e];  // the same for every row: a broadcast
-            sv[4 * e] = mod_score(smod, sv[4 * e] * sl_raw, slope, k4.x - qpos);
-            sv[4 * e + 1] = mod_score(smod, sv[4 * e + 1] * sl_raw, slope, k4.y - qpos);
-            sv[4 * e + 2] = mod_score(smod, sv[4 * e + 2] * sl_raw, slope, k4.z - qpos);
-            sv[4 * e + 3] = mod_score(smod, sv[4 * e + 3] * sl_raw, slope, k4.w - qpos);
-          }
-        }
         // keys without data: -inf (probability 0); scores stay unscaled, the
         // running max is in log2 units; the max as a tree, not a chain
         if (vmask != 0xffffffffu) {
@@ -714,7 +611,7 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
       } else {
         // ---- row `tid`: normalised output and LSE, to o_part or the chunk workspace
         tc05::fence_after_sync();
-        const float inv = lr > 0.f ? (FMT != 0 ? a.v_descale : 1.f) / lr : 0.f;  // E4M3, E2M1: value = code * v_descale
+        const float inv = lr > 0.f ? (F8 ? a.v_descale : 1.f) / lr : 0.f;  // E4M3: value = code * v_descale
         const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         float* dst = nullptr;
         float* ldst = nullptr;
@@ -773,8 +670,8 @@ __global__ void __launch_bounds__(kWThreads, 2) gqa_partial_ext_ws_kernel(const 
   }
 }
 
-template <int D, int G, int FMT, bool MOD>
-int launch_ext_ws_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+template <int D, int G, bool F8>
+static int launch_ext_ws_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   constexpr int QB = kWRows / G;
   const int page_slots = a.chunk / a.ps_l + 2;
   const size_t smem = WsLayout<D>::smem_bytes(page_slots);
@@ -782,7 +679,7 @@ int launch_ext_ws_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   // the copy warps exchange pool row indices as 32-bit values
   if (static_cast<int64_t>(a.P) * a.num_pages * a.num_kv_heads * a.ps_l >= (int64_t{1} << 31))
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  auto kern = gqa_partial_ext_ws_kernel<D, G, FMT, MOD>;
+  auto kern = gqa_partial_ext_ws_kernel<D, G, F8>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
@@ -795,23 +692,34 @@ int launch_ext_ws_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <int D, int FMT, bool MOD>
-int ext_ws_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
+template <int D, bool F8>
+static int ext_ws_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
   switch (G) {
-    case 1: return launch_ext_ws_t<D, 1, FMT, MOD>(a, s, err);
-    case 2: return launch_ext_ws_t<D, 2, FMT, MOD>(a, s, err);
-    case 4: return launch_ext_ws_t<D, 4, FMT, MOD>(a, s, err);
-    case 8: return launch_ext_ws_t<D, 8, FMT, MOD>(a, s, err);
-    case 16: return launch_ext_ws_t<D, 16, FMT, MOD>(a, s, err);
+    case 1: return launch_ext_ws_t<D, 1, F8>(a, s, err);
+    case 2: return launch_ext_ws_t<D, 2, F8>(a, s, err);
+    case 4: return launch_ext_ws_t<D, 4, F8>(a, s, err);
+    case 8: return launch_ext_ws_t<D, 8, F8>(a, s, err);
+    case 16: return launch_ext_ws_t<D, 16, F8>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
 }
 
-template <int FMT, bool MOD>
-int ext_ws_dispatch(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+int launch_gqa_partial_ext(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  // E2M1 pools and modified scores: the two-tile kernel (partial_gqa_pieces.cuh)
+  if (a.kv_fp4) return launch_gqa_pieces_fp4(a, s, err);
+  if (a.has_mod) return a.kv_fp8 ? launch_gqa_pieces_e4m3(a, s, err) : launch_gqa_pieces_bf16(a, s, err);
+  return launch_gqa_partial_ext_ws(a, s, err);
+}
+
+int launch_gqa_partial_ext_ws(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   const int G = a.num_q_heads / a.num_kv_heads;
-  if (a.head_dim == 128) return ext_ws_dispatch_g<128, FMT, MOD>(a, G, s, err);
-  if (a.head_dim == 64) return ext_ws_dispatch_g<64, FMT, MOD>(a, G, s, err);
+  if (a.kv_fp8) {
+    if (a.head_dim == 128) return ext_ws_dispatch_g<128, true>(a, G, s, err);
+    if (a.head_dim == 64) return ext_ws_dispatch_g<64, true>(a, G, s, err);
+    return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (a.head_dim == 128) return ext_ws_dispatch_g<128, false>(a, G, s, err);
+  if (a.head_dim == 64) return ext_ws_dispatch_g<64, false>(a, G, s, err);
   return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }
 

@@ -208,21 +208,21 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
   float mx[NT][2], l[NT][2];  // heads 8 n + 2 qi, + 1
 #pragma unroll
   for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
-  const float sl = a.scale * a.k_descale * (MOD ? 1.f : kLog2e);
+  const float sl = MOD ? 1.f : a.scale * a.k_descale * kLog2e;
   const int krow = f4_row(g8);             // stage rows of keys g8 (+ 8)
   const int vr0 = f4_row(2 * qi), vr1 = f4_row(2 * qi + 1);
   ScoreMod sm_mod;
   float slope[NT][2];
   int qpos = 0;
   if constexpr (MOD) {
-    sm_mod = score_mod_of(a.softcap);
+    sm_mod = score_mod_of(a.softcap, a.scale * a.k_descale);
     qpos = a.slopes != nullptr ? query_pos(a, b, t, t) : 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hd = n * 8 + 2 * qi + e;
-        slope[n][e] = a.slopes != nullptr && hd < G ? __ldg(a.slopes + h * G + hd) : 0.f;
+        slope[n][e] = a.slopes != nullptr && hd < G ? __ldg(a.slopes + h * G + hd) * kLog2e : 0.f;
       }
   }
 

@@ -210,16 +210,16 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
 #pragma unroll
   for (int u = 0; u < NT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  const float sl = a.scale * (MOD ? 1.f : kLog2e) * (F8 ? a.k_descale : 1.f);
+  const float sl = MOD ? 1.f : a.scale * kLog2e * (F8 ? a.k_descale : 1.f);  // MOD: in smod
   ScoreMod smod;
   float slope0 = 0.f, slope1 = 0.f;  // heads quad, quad + 8
   int qpos = 0;
   if constexpr (MOD) {
-    smod = score_mod_of(a.softcap);
+    smod = score_mod_of(a.softcap, a.scale * (F8 ? a.k_descale : 1.f));
     if (a.slopes != nullptr) {
       qpos = query_pos(a, b, t, t);
-      if (quad < G) slope0 = __ldg(a.slopes + h * G + quad);
-      if (quad + 8 < G) slope1 = __ldg(a.slopes + h * G + quad + 8);
+      if (quad < G) slope0 = __ldg(a.slopes + h * G + quad) * kLog2e;
+      if (quad + 8 < G) slope1 = __ldg(a.slopes + h * G + quad + 8) * kLog2e;
     }
   }
   const int mrow = lane & 7;

@@ -198,16 +198,16 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
 #pragma unroll
   for (int u = 0; u < MT; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 qi, 2 qi + 1
-  const float sl = a.scale * (MOD ? 1.f : kLog2e) * (F8 ? a.k_descale : 1.f);
+  const float sl = MOD ? 1.f : a.scale * kLog2e * (F8 ? a.k_descale : 1.f);  // MOD: in smod
   ScoreMod smod;
   float slope0 = 0.f, slope1 = 0.f;  // heads 2 qi, 2 qi + 1
   int qpos = 0;
   if constexpr (MOD) {
-    smod = score_mod_of(a.softcap);
+    smod = score_mod_of(a.softcap, a.scale * (F8 ? a.k_descale : 1.f));
     if (a.slopes != nullptr) {
       qpos = query_pos(a, b, t, t);
-      if (2 * qi < G) slope0 = __ldg(a.slopes + h * G + 2 * qi);
-      if (2 * qi + 1 < G) slope1 = __ldg(a.slopes + h * G + 2 * qi + 1);
+      if (2 * qi < G) slope0 = __ldg(a.slopes + h * G + 2 * qi) * kLog2e;
+      if (2 * qi + 1 < G) slope1 = __ldg(a.slopes + h * G + 2 * qi + 1) * kLog2e;
     }
   }
   const int mrow = lane & 7;

@@ -9,15 +9,28 @@
 
 namespace cpattn {
 
+// Kinds of cap: none; up to kPlainCap, where tanh(y) = 1 - 2 / (e^{2 y} + 1)
+// with the approximate ex2 and reciprocal (2^-22 and 2^-23 relative) is off by
+// at most cap * 2^-21, 3e-5; larger ones, where that error would show in the
+// log-sum-exp and |y| < 0.2 takes the series up to y^7 instead (the next term,
+// 62 y^9 / 2835, is below 6e-8 of y there): about 2^-20 relative everywhere.
+// Both ends come out as +-cap (e = inf, e = 0).  The hardware's own tanh is off
+// by 2^-11 of its result.
+enum : int { kCapNone = 0, kCapPlain = 1, kCapSeries = 2 };
+constexpr float kPlainCap = 64.f;
+
 struct ScoreMod {
-  float cap;  // 0: no cap
-  float inv;  // 1 / cap
+  int kind;
+  float lin;     // score s of a raw product: s log2 e (no cap), 2 s log2 e / cap (plain), s / cap (series)
+  float top;     // cap * log2 e
 };
 
-__device__ __forceinline__ ScoreMod score_mod_of(float softcap) {
+// `scale`: natural-domain score of a raw dot product (descales included)
+__device__ __forceinline__ ScoreMod score_mod_of(float softcap, float scale) {
   ScoreMod m;
-  m.cap = softcap;
-  m.inv = softcap > 0.f ? 1.f / softcap : 0.f;
+  m.kind = softcap <= 0.f ? kCapNone : (softcap <= kPlainCap ? kCapPlain : kCapSeries);
+  m.top = softcap * kLog2e;
+  m.lin = m.kind == kCapNone ? scale * kLog2e : (m.kind == kCapPlain ? 2.f * kLog2e * scale / softcap : scale / softcap);
   return m;
 }
 
@@ -27,23 +40,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(y) to about 2^-20 relative: for |y| < 0.2 the series up to y^7 (the
-// next term, 62 y^9 / 2835, is below 6e-8 of y there), else
-// 1 - 2 / (e^{2 y} + 1) with the approximate ex2 and reciprocal (2^-22 and
-// 2^-23 relative).  Both ends come out as +-1 (e = inf, e = 0).  The hardware's
-// own tanh is off by 2^-11 of its result, which the log-sum-exp would show.
-__device__ __forceinline__ float tanh_fast(float y) {
+// Capped (or only scaled) score in the log2 domain from the raw product.
+template <int KIND>
+__device__ __forceinline__ float cap_score(const ScoreMod& m, float raw) {
+  const float y = raw * m.lin;
+  if constexpr (KIND == kCapNone) return y;
+  if constexpr (KIND == kCapPlain) return fmaf(-2.f * m.top, rcp_approx(ex2_approx(y) + 1.f), m.top);
   const float y2 = y * y;
-  const float series =
-      fmaf(y * y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), y);
+  const float series = fmaf(y * y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), y);
   const float e = ex2_approx(y * (2.f * kLog2e));
-  return fabsf(y) < 0.2f ? series : fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+  return m.top * (fabsf(y) < 0.2f ? series : fmaf(-2.f, rcp_approx(e + 1.f), 1.f));
 }
 
-// Modified score in the log2 domain from the scaled score x.
-__device__ __forceinline__ float mod_score(const ScoreMod& m, float x, float slope, float away) {
-  if (m.cap > 0.f) x = m.cap * tanh_fast(x * m.inv);
-  return fmaf(slope, away, x) * kLog2e;
+// Modified score in the log2 domain; slope2 = slope * log2 e, away = key's minus query's position.
+__device__ __forceinline__ float mod_score(const ScoreMod& m, float raw, float slope2, float away) {
+  const float x = m.kind == kCapNone ? cap_score<kCapNone>(m, raw)
+                  : m.kind == kCapPlain ? cap_score<kCapPlain>(m, raw) : cap_score<kCapSeries>(m, raw);
+  return fmaf(slope2, away, x);
 }
 
 // Logical position of partner p's stripe slot k.

@@ -55,7 +55,8 @@
  *   stored as zeros, and one that holds a NaN reads as NaN.  At head_dim 128
  *   a row takes 72 bytes (bf16: 256).  head_dim must be a multiple of 32.
  *   Queries over E4M3 and E2M1 pools are multiplied as float16 (exact for
- *   magnitudes in [2^-14, 65504]) in rows of one token, as bf16 otherwise.
+ *   magnitudes in [2^-14, 65504]), but for rows of several tokens over E4M3
+ *   pools with unmodified scores, which take them as bf16.
  *   Partial outputs and log-sum-exps are always fp32.  Log-sum-exps use the
  *   natural logarithm; an empty key set gives output 0 and LSE -inf.
  *
