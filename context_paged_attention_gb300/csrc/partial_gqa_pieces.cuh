@@ -365,9 +365,12 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       const int nst = is_k ? kKStages : kVStages;
       uint8_t* ring = is_k ? sK : sV;
       const int b_full = is_k ? B_KFULL : B_VFULL, b_free = is_k ? B_KFREE : B_VFREE;
-      // the lane's key of each tile: slot k of partner pp, 64 slots further a tile
+      // The lane's key of each tile: slot k of partner pp.  Tiles go from the
+      // last to the first, a partner's keys from the nearest back: scores that
+      // fall with the distance then meet their maximum at once (front to back
+      // raised it, and rescaled O, at almost every tile of a steep head).
       const int x0 = unit * kUnit + lane;
-      int pp = x0 / len, k = kb + x0 - pp * len;
+      int pp = ((ntiles - 1) * kTile + x0) / len, k = kb + (ntiles - 1) * kTile + x0 - pp * len;
       int n_pp = stripe_len(L, p0 + min(pp, np - 1), P, a.interleave);
       // pool row of the lane's key of the next tile (-1: no key), its position; advances the key
       auto next_row = [&](float& pos) -> int {
@@ -380,10 +383,10 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
                                    (k - j * a.ps_l));
           if (MOD && is_k) pos = static_cast<float>(stripe_pos(k, p0 + pp, P, a.interleave));
         }
-        k += kTile;
-        while (pp < np && k >= kb + len) {
-          k -= len;
-          ++pp;
+        k -= kTile;
+        while (k < kb && pp > 0) {
+          k += len;
+          --pp;
           n_pp = stripe_len(L, p0 + min(pp, np - 1), P, a.interleave);
         }
         return row;
