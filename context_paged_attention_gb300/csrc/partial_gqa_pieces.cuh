@@ -32,8 +32,9 @@
 // barrier's own suspended wait: polling took a third of the issue slots.
 // (Two threads a row, 16 softmax warps, was slower: half the keys a thread
 // with the same waits and barriers, 340 instructions a warp for 32 keys.)
-// Tensor memory (512 columns, one CTA an SM), tile t at 256 t: S 64 columns,
-// P two buffers of 32, O head_dim columns.  Every wait is bounded; one that
+// Tensor memory (512 columns, one CTA an SM), tile t at 256 t: two S buffers of
+// 64 columns, O head_dim columns; P of a key tile overwrites the first 32
+// columns of its S, so S of the tile after next waits for P V of this one.  Every wait is bounded; one that
 // runs out raises the CTA's abort flag, which ends every other wait, and the
 // call reports CPATTN_DEV_TC_TIMEOUT.
 //
@@ -71,9 +72,8 @@ constexpr int B_KFULL = 0;                    // [64 lanes (cp.async) or 2 warps
 constexpr int B_KFREE = B_KFULL + kKStages;   // [commit] x4
 constexpr int B_VFULL = B_KFREE + kKStages;   // [as K] x3
 constexpr int B_VFREE = B_VFULL + kVStages;   // [commit] x3
-constexpr int B_SDONE = B_VFREE + kVStages;   // [commit] x2 tiles
-constexpr int B_SFREE = B_SDONE + 2;          // [4 warps] x2
-constexpr int B_PFULL = B_SFREE + 2;          // [4 warps] x2 tiles x2 buffers
+constexpr int B_SDONE = B_VFREE + kVStages;   // [commit] x2 tiles x2 buffers
+constexpr int B_PFULL = B_SDONE + 4;          // [4 warps] x2 x2
 constexpr int B_PVDONE = B_PFULL + 4;         // [commit] x2 x2
 constexpr int B_Q = B_PVDONE + 4;             // [the softmax warps of the tiles with tokens]
 constexpr int B_FIN = B_Q + 1;                // [commit] x2 issuing warps
@@ -86,7 +86,7 @@ struct Layout {
   static constexpr int QTILE = KB * QBLK;
   static constexpr int BLK = kTile * 128;
   static constexpr int TILE = KB * BLK;
-  static constexpr uint32_t P_COL = 64, O_COL = 128, TILE_COLS = 256, TMEM_COLS = 512;
+  static constexpr uint32_t S_COLS = 64, O_COL = 128, TILE_COLS = 256, TMEM_COLS = 512;
   static constexpr size_t OFF_K = 2 * QTILE;
   static constexpr size_t OFF_V = OFF_K + static_cast<size_t>(kKStages) * TILE;
   static constexpr size_t OFF_BAR = OFF_V + static_cast<size_t>(kVStages) * TILE;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       for (int i = 0; i < B_COUNT; ++i) {
         uint32_t cnt = 1;
         if (i < B_KFREE || (i >= B_VFULL && i < B_VFREE)) cnt = F16 ? kUnits : 32 * kUnits;
-        if (i >= B_SFREE && i < B_PVDONE) cnt = 4;
+        if (i >= B_PFULL && i < B_PVDONE) cnt = 4;
         if (i == B_Q) cnt = 4 * ntl;
         tc05::mbar_init(bar(i), cnt);
       }
@@ -461,23 +461,30 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
             const int key = unit * kUnit + u * RPI + ro;
             const uint32_t on = ((now.valid >> (u * RPI + ro)) & 1u) ? 0xffffffffu : 0u;
             const uint32_t w[4] = {now.codes[u].x & on, now.codes[u].y & on, now.codes[u].z & on, now.codes[u].w & on};
+            // Pieces 8 apart lie in different column blocks at the same banks: the
+            // lanes of the upper block take their pieces in another order, so the
+            // eight lanes of a store phase hit all banks.
+            const bool upper = cq >= CHQ / (D / 64);
             if constexpr (FMT == kFp4) {
               const uint32_t s2 = e4m3x2_to_f16x2(now.scl[u] & on);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {  // 8 codes: one 16-byte piece of the row
+              for (int x0 = 0; x0 < 4; ++x0) {  // 8 codes: one 16-byte piece of the row
+                const int x = upper ? x0 ^ 2 : x0;
+                const uint32_t wx = upper ? w[x0 ^ 2] : w[x0];
                 const uint32_t sb = __byte_perm(s2, 0u, x < 2 ? 0x1010u : 0x3232u);
                 const int cb = 4 * cq + x;
                 *reinterpret_cast<uint4*>(dst0 + (cb >> 3) * Lt::BLK + tc05::sw128(key, cb & 7)) =
-                    make_uint4(mul_f16x2(e2m1x2_to_f16x2<0>(w[x]), sb), mul_f16x2(e2m1x2_to_f16x2<1>(w[x]), sb),
-                               mul_f16x2(e2m1x2_to_f16x2<2>(w[x]), sb), mul_f16x2(e2m1x2_to_f16x2<3>(w[x]), sb));
+                    make_uint4(mul_f16x2(e2m1x2_to_f16x2<0>(wx), sb), mul_f16x2(e2m1x2_to_f16x2<1>(wx), sb),
+                               mul_f16x2(e2m1x2_to_f16x2<2>(wx), sb), mul_f16x2(e2m1x2_to_f16x2<3>(wx), sb));
               }
             } else {
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int cb = 2 * cq + x;
+              for (int x0 = 0; x0 < 2; ++x0) {
+                const int cb = 2 * cq + (upper ? x0 ^ 1 : x0);
+                const uint32_t c0 = upper ? w[2 * (x0 ^ 1)] : w[2 * x0], c1 = upper ? w[2 * (x0 ^ 1) + 1] : w[2 * x0 + 1];
                 *reinterpret_cast<uint4*>(dst0 + (cb >> 3) * Lt::BLK + tc05::sw128(key, cb & 7)) =
-                    make_uint4(e4m3x2_to_f16x2(w[2 * x]), e4m3x2_to_f16x2(w[2 * x] >> 16),
-                               e4m3x2_to_f16x2(w[2 * x + 1]), e4m3x2_to_f16x2(w[2 * x + 1] >> 16));
+                    make_uint4(e4m3x2_to_f16x2(c0), e4m3x2_to_f16x2(c0 >> 16), e4m3x2_to_f16x2(c1),
+                               e4m3x2_to_f16x2(c1 >> 16));
               }
             }
           }
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       const uint32_t bar0 = bar(0);
       bool issued = false;
       if (warp == kSWarp) {
-        // S of each key tile for every query tile, as soon as the softmax has read the last one
+        // S of each key tile for every query tile, as soon as P V of the tile before last has read its buffer
         constexpr uint32_t id_s = F16 ? tc05::idesc_f16(128, kTile, false, false) : tc05::idesc_bf16(128, kTile, false, false);
         const uint64_t dq = tc05::desc_k128(tc05::smem_addr(base));
         const uint64_t dk0 = tc05::desc_k128(tc05::smem_addr(sK));
@@ -515,15 +522,15 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t < ntl && alive) {
-              if (j > 0) alive = wait_phase(bar0 + 8 * (B_SFREE + t), (j - 1) & 1, s_abort);
+              if (j > 1) alive = wait_phase(bar0 + 8 * (B_PVDONE + 2 * t + (j & 1)), ((j >> 1) - 1) & 1, s_abort);
               tc05::fence_after_sync();
               if (alive && tc05::elect_one()) {
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
-                  tc05::mma_ss(tbase + t * Lt::TILE_COLS,
+                  tc05::mma_ss(tbase + t * Lt::TILE_COLS + Lt::S_COLS * (j & 1),
                                tc05::desc_add(dq, t * Lt::QTILE + (s >> 2) * Lt::QBLK + (s & 3) * 32),
                                tc05::desc_add(dk, (s >> 2) * Lt::BLK + (s & 3) * 32), id_s, s > 0);
-                tc05::commit(bar0 + 8 * (B_SDONE + t));
+                tc05::commit(bar0 + 8 * (B_SDONE + 2 * t + (j & 1)));
                 if (t == ntl - 1) tc05::commit(bar0 + 8 * (B_KFREE + st));
               }
               __syncwarp();
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
               if (alive && tc05::elect_one()) {
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                  tc05::mma_ts(tt + Lt::O_COL, tt + Lt::P_COL + 32 * (j & 1) + 8 * s, tc05::desc_add(dv, s * 16 * 128),
+                  tc05::mma_ts(tt + Lt::O_COL, tt + Lt::S_COLS * (j & 1) + 8 * s, tc05::desc_add(dv, s * 16 * 128),
                                id_o, j > 0 || s > 0);
                 tc05::commit(bar0 + 8 * (B_PVDONE + 2 * t + (j & 1)));
                 if (t == ntl - 1) tc05::commit(bar0 + 8 * (B_VFREE + st));
@@ -607,17 +614,18 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       }
       for (int i = 0; i < ntiles; ++i) {
         const int bb = i & 1;
-        bool ok = wait_phase(bar(B_SDONE + my_t), i & 1, s_abort);
+        bool ok = wait_phase(bar(B_SDONE + 2 * my_t + bb), (i >> 1) & 1, s_abort);
         if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
         tc05::fence_after_sync();
         const uint32_t mlo = smask[(i % kMaskSlots) * kUnits], mhi = smask[(i % kMaskSlots) * kUnits + 1];
+        const uint32_t s_lane = my_lane + Lt::S_COLS * bb;
         float sv[kTile];
         {
           float v0[16], v1[16], v2[16], v3[16];
-          tc05::ld_x16(my_lane, v0);
-          tc05::ld_x16(my_lane + 16, v1);
-          tc05::ld_x16(my_lane + 32, v2);
-          tc05::ld_x16(my_lane + 48, v3);
+          tc05::ld_x16(s_lane, v0);
+          tc05::ld_x16(s_lane + 16, v1);
+          tc05::ld_x16(s_lane + 32, v2);
+          tc05::ld_x16(s_lane + 48, v3);
           tc05::ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -627,9 +635,6 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
             sv[48 + e] = v3[e];
           }
         }
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) ws_arrive(bar(B_SFREE + my_t));
         if constexpr (MOD) {
           const float4* kp = reinterpret_cast<const float4*>(spos + (i % kMaskSlots) * kTile);
           if (a.slopes == nullptr) {
@@ -661,7 +666,8 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
         const float bm = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sl;
         const bool up = bm > m + 8.f;
         if (__any_sync(0xffffffffu, up) && i > 0) {
-          // rescale O rows whose max rose; P V of the previous tile must be done
+          // rescale O rows whose max rose; P V of the previous tile must be done (S of this tile came after
+          // P V of the tile before it, so the wait cannot see an older phase)
           ok = wait_phase(bar(B_PVDONE + 2 * my_t + ((i - 1) & 1)), ((i - 1) >> 1) & 1, s_abort);
           if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
           tc05::fence_after_sync();
@@ -679,11 +685,6 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
           l *= alpha;
         }
         if (up) m = bm;
-        // P(i) into its buffer once P V of tile i-2 no longer reads it
-        if (i >= 2) {
-          ok = wait_phase(bar(B_PVDONE + 2 * my_t + bb), ((i - 2) >> 1) & 1, s_abort);
-          if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
-        }
         // one FMA and one ex2 a key (-inf gives 0; while every key so far is
         // masked m is -inf and every p is 0)
         const float nm = m == -INFINITY ? 0.f : -m;
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
             ls[e & 1] = add2(ls[e & 1], pair2(pa, pb));
             pk[e] = pack16<F16>(pa, pb);
           }
-          tc05::st_x16_u32(my_lane + Lt::P_COL + 32 * bb + 16 * hh, pk);
+          tc05::st_x16_u32(s_lane + 16 * hh, pk);
         }
         {
           float s0, s1;
@@ -839,79 +840,107 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   if (tid == 0) a.ws_cnt[slot0] = 0;
 }
 
-// Fused calls: the exact merge of a row's pieces and the extra partial, a warp
-// a (token, query head).  Its own kernel, because a block's last CTA alone took
-// 34 us for the 256 rows of its merge (a row of E pieces is E + 1 short reads,
-// which one SM cannot keep enough of in flight).
+// Fused calls: the exact merge of a row's pieces and the extra partial, a block
+// a token and a warp two of its heads at a time.  Its own kernel, because a
+// block's last CTA alone took 34 us for the 256 rows of its merge (a row of E
+// pieces is E + 1 short reads, which one SM cannot keep enough of in flight).
+// What it spends is the chain of dependent small reads (row, length, LSEs,
+// values), so blocks are many and light: four heads a warp at 128 registers
+// took 35 us for 2064 tokens.
 template <int D>
-__global__ void __launch_bounds__(256) gqa_pieces_merge_kernel(const PartialArgs a, const pieces::Geo geo, int G) {
+__global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialArgs a, const pieces::Geo geo, int G) {
   pdl_wait();
+  constexpr int NH = 2;            // heads a warp merges together
   constexpr int LN = D / 4;        // lanes a row takes
   constexpr int PARTS = 32 / LN;   // pieces read at once
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int t = static_cast<int>(row / a.num_q_heads);
-  if (t >= a.num_tokens || t >= __ldg(a.qo_indptr + a.num_rows)) return;
-  const int hq = static_cast<int>(row - static_cast<int64_t>(t) * a.num_q_heads);
-  const int b = find_row(a.qo_indptr, a.num_rows, t);
-  if (__ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b) < 2) return;  // one-token rows: the decode kernel's
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x;
+  const int b = find_row_warp(a.qo_indptr, a.num_rows, t);
+  if (b < 0 || __ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b) < 2) return;  // one-token rows: the decode kernel's
   const int L = min(__ldg(a.kv_len + b), a.max_kv_len);
   const int E = (L + geo.run - 1) / geo.run;
   if (E < 2) return;
-  const int64_t w0 = (static_cast<int64_t>(t) * a.num_kv_heads + hq / G) * geo.max_runs * G + hq % G;  // piece e: w0 + e G
-  const float le = a.extra_lse != nullptr ? __ldg(a.extra_lse + row) : -INFINITY;
-  float mx = le;
-  for (int e = lane; e < E; e += 32) mx = fmaxf(mx, __ldg(geo.ws_lse + w0 + static_cast<int64_t>(e) * G));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float mm = mx == -INFINITY ? 0.f : mx;  // no keys anywhere: every weight 0
-  float sum = 0.f;
   const int part = lane / LN, c4 = lane - part * LN;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const float we = e0 + lane < E ? expf(__ldg(geo.ws_lse + w0 + static_cast<int64_t>(e0 + lane) * G) - mm) : 0.f;
-    sum += we;
-    const int n = min(32, E - e0);
-#pragma unroll 4
-    for (int e = part; e < n + PARTS - 1; e += PARTS) {
-      const float x = __shfl_sync(0xffffffffu, we, e & 31);
-      if (e < n && x != 0.f) {  // an empty piece's row is never read
-        const float4 v = __ldg(reinterpret_cast<const float4*>(geo.ws_o + (w0 + static_cast<int64_t>(e0 + e) * G) * D) + c4);
-        acc.x = fmaf(x, v.x, acc.x);
-        acc.y = fmaf(x, v.y, acc.y);
-        acc.z = fmaf(x, v.z, acc.z);
-        acc.w = fmaf(x, v.w, acc.w);
+  for (int h0 = warp * NH; h0 < a.num_q_heads; h0 += (blockDim.x >> 5) * NH) {
+    int64_t w0[NH], row[NH];  // piece e of head i: workspace row w0 + e G
+    float le[NH], mx[NH], sum[NH];
+    float4 acc[NH], vx[NH];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int hq = min(h0 + i, a.num_q_heads - 1);  // past the last head: its work again, not written
+      row[i] = static_cast<int64_t>(t) * a.num_q_heads + hq;
+      w0[i] = (static_cast<int64_t>(t) * a.num_kv_heads + hq / G) * geo.max_runs * G + hq % G;
+      le[i] = a.extra_lse != nullptr ? __ldg(a.extra_lse + row[i]) : -INFINITY;
+      vx[i] = acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      mx[i] = le[i];
+      for (int e = lane; e < E; e += 32) mx[i] = fmaxf(mx[i], __ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e) * G));
+      if (le[i] != -INFINITY) vx[i] = __ldg(reinterpret_cast<const float4*>(a.extra_o + row[i] * D) + c4);
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+      if (mx[i] == -INFINITY) mx[i] = 0.f;  // no keys anywhere: every weight 0
+    }
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      float we[NH];
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        we[i] = e0 + lane < E ? expf(__ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e0 + lane) * G) - mx[i]) : 0.f;
+        sum[i] += we[i];
+      }
+      const int n = min(32, E - e0);
+#pragma unroll 2
+      for (int eb = 0; eb < n; eb += PARTS) {
+        const int e = eb + part;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          const float x = __shfl_sync(0xffffffffu, we[i], e & 31);
+          if (e < n && x != 0.f) {  // an empty piece's row is never read
+            const float4 v =
+                __ldg(reinterpret_cast<const float4*>(geo.ws_o + (w0[i] + static_cast<int64_t>(e0 + e) * G) * D) + c4);
+            acc[i].x = fmaf(x, v.x, acc[i].x);
+            acc[i].y = fmaf(x, v.y, acc[i].y);
+            acc[i].z = fmaf(x, v.z, acc[i].z);
+            acc[i].w = fmaf(x, v.w, acc[i].w);
+          }
+        }
       }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if constexpr (PARTS == 2) {
-    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    for (int i = 0; i < NH; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      if constexpr (PARTS == 2) {
+        acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, 16);
+        acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, 16);
+        acc[i].z += __shfl_xor_sync(0xffffffffu, acc[i].z, 16);
+        acc[i].w += __shfl_xor_sync(0xffffffffu, acc[i].w, 16);
+      }
+      const float wx = le[i] == -INFINITY ? 0.f : expf(le[i] - mx[i]);
+      acc[i].x = fmaf(wx, vx[i].x, acc[i].x);
+      acc[i].y = fmaf(wx, vx[i].y, acc[i].y);
+      acc[i].z = fmaf(wx, vx[i].z, acc[i].z);
+      acc[i].w = fmaf(wx, vx[i].w, acc[i].w);
+      sum[i] += wx;
+      if (h0 + i >= a.num_q_heads) continue;
+      const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
+      if (part == 0) {
+        const int64_t oi = row[i] * D + c4 * 4;
+        if (a.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + oi) =
+              make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + oi) =
+              make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+      }
+      if (lane == 0 && a.lse_out != nullptr) a.lse_out[row[i]] = sum[i] > 0.f ? mx[i] + logf(sum[i]) : -INFINITY;
+    }
   }
-  const float wx = le == -INFINITY ? 0.f : expf(le - mm);
-  if (wx != 0.f) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(a.extra_o + row * D) + c4);
-    acc.x = fmaf(wx, v.x, acc.x);
-    acc.y = fmaf(wx, v.y, acc.y);
-    acc.z = fmaf(wx, v.z, acc.z);
-    acc.w = fmaf(wx, v.w, acc.w);
-  }
-  sum += wx;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (part == 0) {
-    const int64_t oi = row * D + c4 * 4;
-    if (a.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + oi) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + oi) =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  }
-  if (lane == 0 && a.lse_out != nullptr) a.lse_out[row] = sum > 0.f ? mm + logf(sum) : -INFINITY;
 }
 
 namespace pieces {
@@ -952,9 +981,7 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   kern<<<grid, kThreads, smem, s>>>(a, geo);
   *err = cudaGetLastError();
   if (*err == cudaSuccess && a.fused && geo.max_runs > 1) {
-    const int64_t rows = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
-    if ((rows + 7) / 8 > 0x7fffffff) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-    *err = launch_pdl(gqa_pieces_merge_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a, geo, G);
+    *err = launch_pdl(gqa_pieces_merge_kernel<D>, dim3(a.num_tokens), dim3(256), 0, s, a, geo, G);
   }
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
