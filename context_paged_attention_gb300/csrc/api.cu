@@ -127,7 +127,7 @@ size_t partial_workspace(const cpattn_pool_desc* desc, int fused, int32_t num_q_
   if (check_desc(desc) != CPATTN_OK || num_q_heads < 1 || num_tokens < 0 || max_kv_len < 0) return 0;
   if (num_q_heads % desc->num_kv_heads != 0) return 0;
   PartialPlan plan;
-  if (!plan_partial(is_mla(desc), fused, desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads,
+  if (!plan_partial(is_mla(desc), fused, is_fp4(desc), desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads,
                     num_q_heads, desc->head_dim, num_tokens, max_kv_len, dtype_bytes(desc->dtype), &plan))
     return 0;
   return plan.bytes();
@@ -167,7 +167,7 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
 
   PartialPlan plan;
-  if (!plan_partial(mla, f.fused, desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads, num_q_heads,
+  if (!plan_partial(mla, f.fused, is_fp4(desc), desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads, num_q_heads,
                     desc->head_dim, num_tokens, max_kv_len, dtype_bytes(desc->dtype), &plan))
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
   const size_t need = plan.bytes();
@@ -230,6 +230,10 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.seg = plan.seg;
   a.chunk = plan.chunk;
   a.max_chunks = plan.max_chunks;
+  a.run = plan.run;
+  a.max_runs = plan.max_runs;
+  a.ws_run_o = ws_part;
+  a.ws_run_lse = ws_part_lse;
   a.scale = scale;
   a.kv_fp8 = is_fp8(desc);
   a.kv_fp4 = is_fp4(desc);

@@ -125,6 +125,11 @@ struct PartialArgs {
   void* out;               // [T][Hq][Dv], bf16 when out_bf16 else fp32
   int out_bf16;
   float* lse_out;          // [T][Hq] or null
+  // fused calls over E2M1 pools: runs of `run` logical positions (whole pages), every partner's keys of a run
+  // in one CTA; pieces [T * Hkv][max_runs][G][Dv] and their LSEs of rows of several runs
+  int run, max_runs;
+  float* ws_run_o;
+  float* ws_run_lse;
   // score modification (has_mod): s = scale q.k, capped by softcap * tanh(s / softcap)
   // when softcap > 0, plus slopes[query head] * (key position - query position)
   int has_mod;
@@ -144,10 +149,11 @@ struct PartialPlan {
   int seg, chunk, max_chunks;
   size_t ws_o_floats, ws_lse_floats, ws_cnt_ints;
   size_t ws_part_floats, ws_part_lse_floats, ws_pair_ints;  // fused calls: partner partials, pair tickets
+  int run, max_runs;  // fused calls over E2M1 pools: page runs (their pieces take the partner partials' place)
   size_t bytes() const;
 };
 // Returns false if the shape is unsupported.
-bool plan_partial(int mla, int fused, int P, int interleave, int page_size, int num_kv_heads, int num_q_heads, int head_dim,
+bool plan_partial(int mla, int fused, int fp4, int P, int interleave, int page_size, int num_kv_heads, int num_q_heads, int head_dim,
                   int num_tokens, int max_kv_len, int dtype_bytes, PartialPlan* plan);
 
 // status: 0 ok, CPATTN_ERR_UNSUPPORTED_SHAPE, or the cudaError via *err

@@ -246,7 +246,20 @@ size_t PartialPlan::bytes() const {
          al(ws_part_lse_floats * 4) + al(ws_pair_ints * 4);
 }
 
-bool plan_partial(int mla, int fused, int P, int interleave, int page_size, int num_kv_heads, int num_q_heads, int head_dim,
+// Positions of a run of a fused call over an E2M1 pool, in whole pages: one
+// round of CTAs (four an SM) when every row has max_kv_len keys, within
+// [512, 4096].  A CTA's start and end take some 10 us beside its neighbours'
+// work: 64 rows of 512-8192 keys took 126, 103, 93 and 86 us at runs of 512,
+// 1024, 2048 and 4096 (8 rows of 64k-128k: 458, 312, 246, 227), while few rows
+// need the split to reach every SM.
+static int fp4_fused_run(int page_size, int num_kv_heads, int num_tokens, int max_kv_len) {
+  constexpr int kCtas = 4 * 152;
+  const int64_t want = (static_cast<int64_t>(num_tokens) * num_kv_heads * max_kv_len + kCtas - 1) / kCtas;
+  const int run = want < 512 ? 512 : (want > 4096 ? 4096 : static_cast<int>(want));
+  return (run + page_size - 1) / page_size * page_size;
+}
+
+bool plan_partial(int mla, int fused, int fp4, int P, int interleave, int page_size, int num_kv_heads, int num_q_heads, int head_dim,
                   int num_tokens, int max_kv_len, int dtype_bytes, PartialPlan* plan) {
   (void)head_dim;
   const int ps_l = page_size / P;
@@ -254,6 +267,7 @@ bool plan_partial(int mla, int fused, int P, int interleave, int page_size, int 
   const int Dv = mla ? 512 : head_dim;
   plan->seg = pick_seg(ps_l, mla ? 16 : kSegMax);
   const int max_stripe = max_stripe_len(max_kv_len, P, interleave);
+  plan->run = plan->max_runs = 0;
   if (mla) {
     // the MLA kernel plans on the device (stripes longest first, long ones cut
     // into pieces); the workspace holds the pieces' partials, max_chunks of
@@ -311,6 +325,14 @@ bool plan_partial(int mla, int fused, int P, int interleave, int page_size, int 
     plan->ws_part_floats = slots * G * Dv;
     plan->ws_part_lse_floats = slots * G;
     plan->ws_pair_ints = static_cast<size_t>(num_tokens) * num_kv_heads;
+    if (fp4) {
+      plan->run = fp4_fused_run(page_size, num_kv_heads, num_tokens, max_kv_len);
+      plan->max_runs = max_kv_len > 0 ? (max_kv_len + plan->run - 1) / plan->run : 1;
+      if (plan->max_runs + 2 > 3000) return false;
+      const size_t pieces = static_cast<size_t>(num_tokens) * num_kv_heads * plan->max_runs * G;
+      if (pieces * Dv > plan->ws_part_floats) plan->ws_part_floats = pieces * Dv;
+      if (pieces > plan->ws_part_lse_floats) plan->ws_part_lse_floats = pieces;
+    }
   } else {
     plan->ws_part_floats = plan->ws_part_lse_floats = plan->ws_pair_ints = 0;
   }

@@ -6,7 +6,11 @@
 // merge are those of the bf16 decode kernel (CTA = chunk of partner p's stripe
 // of row b for KV head h; stripe slot k at page k / (page_size / P), slot
 // k % (page_size / P) -- mstar PR #1124 "Context / Sequence Parallel 1/5",
-// description).
+// description).  Fused calls are grouped differently: a CTA takes every
+// partner's keys of a run of logical pages (softmax does not mind the order:
+// partner 0's slots, then partner 1's, ...), so no partner partials are written
+// or merged; a row of one run leaves the CTA as final output, longer rows leave
+// pieces that the row's last CTA merges (run length: fp4_fused_run).
 //
 // Heads on the N side of mma.sync m16n8k16, keys (S^T = K Q^T) and dims
 // (O^T = V^T P^T) on the M side.  The order of the MMA's k index (dims of S,
@@ -79,9 +83,10 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
   constexpr uint32_t NOROW = 0xffffffffu;  // the launch checks that rows fit 32 bits
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_vmask[NW][NST];
+  __shared__ int s_pos[MOD ? NW : 1][MOD ? NST : 1][MOD ? KT : 1];  // positions of a stage's keys
 
   const int c = blockIdx.x;
-  const int p = blockIdx.y / a.num_kv_heads;
+  const int p = a.fused ? 0 : blockIdx.y / a.num_kv_heads;  // fused: partners 0 .. P - 1
   const int h = blockIdx.y - p * a.num_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = a.P;
@@ -101,12 +106,23 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
     if (c == 0 && threadIdx.x == 0) report(a.dev_status, CPATTN_DEV_POS_PAST_TABLE);
     L = a.max_kv_len;
   }
-  const int n_p = stripe_len(L, p, P, a.interleave);
-  const int nchunks = n_p > 0 ? (n_p + a.chunk - 1) / a.chunk : 1;
+  // this CTA's keys: stripe slots [kb, kb + len) of np partners from p on
+  int nchunks, kb, len, np;
+  if (a.fused) {
+    nchunks = max(1, (L + a.run - 1) / a.run);
+    const int page0 = c * (a.run / a.page_size);
+    kb = page0 * a.ps_l;
+    len = max(0, min(a.run / a.page_size, (L + a.page_size - 1) / a.page_size - page0)) * a.ps_l;
+    np = P;
+  } else {
+    const int n_p = stripe_len(L, p, P, a.interleave);
+    nchunks = n_p > 0 ? (n_p + a.chunk - 1) / a.chunk : 1;
+    kb = c * a.chunk;
+    len = max(0, min(n_p - kb, a.chunk));
+    np = 1;
+  }
   if (c >= nchunks) return;
-  const int k_begin = c * a.chunk;
-  const int k_end = min(n_p, k_begin + a.chunk);
-  const int nstage = k_end > k_begin ? (k_end - k_begin + KT - 1) / KT : 0;
+  const int nstage = (np * len + KT - 1) / KT;
   const int my_n = nstage > warp ? (nstage - warp + NW - 1) / NW : 0;
 
   // Q as the B operand: head g8 (+ 8), dims q D/4 + 4 m .. + 3 of MMA m
@@ -134,9 +150,9 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
 
   // page ids of the chunk, checked once
   int* spg = reinterpret_cast<int*>(smem + SM::RING);
-  const int j0 = k_begin / a.ps_l;
+  const int j0 = kb / a.ps_l;
   if (nstage > 0) {
-    const int j1 = (k_end - 1) / a.ps_l;
+    const int j1 = (kb + len - 1) / a.ps_l;
     const int pb = __ldg(a.page_indptr + b);
     const int npages = __ldg(a.page_indptr + b + 1) - pb;
     for (int x = threadIdx.x; x <= j1 - j0; x += blockDim.x) {
@@ -155,20 +171,34 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
     }
   }
   __syncthreads();
-  const uint32_t head_row0 = (static_cast<uint32_t>(p) * a.num_pages * a.num_kv_heads + h) * a.ps_l;
   const uint32_t page_rows = static_cast<uint32_t>(a.num_kv_heads) * a.ps_l;
+  const uint32_t partner_rows = static_cast<uint32_t>(a.num_pages) * page_rows;
+  // the lane's key of the warp's next stage: slot k of partner p + pp, NW * KT slots further a stage
+  int pp = 0, k = kb + warp * KT + lane, n_pp = stripe_len(L, p, P, a.interleave);
+  auto settle = [&]() {  // k past this partner's slots: on to the next one's
+    while (k >= kb + len && pp < np) {
+      k -= len;
+      ++pp;
+      n_pp = stripe_len(L, p + min(pp, np - 1), P, a.interleave);
+    }
+  };
+  if (nstage > 0) settle();
 
   // stage i of this warp: lane = key resolves its row and copies its scales,
   // the codes go 32 consecutive chunks an instruction
   auto issue = [&](int i) {
     if (i < my_n) {
-      const int k = k_begin + (warp + i * NW) * KT + lane;
       uint32_t myrow = NOROW;
-      if (k < k_end) {
+      if (pp < np && k < n_pp) {
         const int j = page_of_slot(a, k);
         const int pg = spg[j - j0];
-        if (pg >= 0) myrow = head_row0 + static_cast<uint32_t>(pg) * page_rows + static_cast<uint32_t>(k - j * a.ps_l);
+        if (pg >= 0)
+          myrow = static_cast<uint32_t>(p + pp) * partner_rows + static_cast<uint32_t>(pg) * page_rows +
+                  static_cast<uint32_t>(h * a.ps_l + k - j * a.ps_l);
+        if constexpr (MOD) s_pos[warp][i % NST][lane] = stripe_pos(k, p + pp, P, a.interleave);
       }
+      k += NW * KT;
+      settle();
       const uint32_t vm = __ballot_sync(0xffffffffu, myrow != NOROW);
       if (lane == 0) s_vmask[warp][i % NST] = vm;
       uint8_t* sk = ring + (i % NST) * SM::STAGE;
@@ -277,6 +307,7 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
       }
     }
     // ---- scores in log2 units, masked; the running max over the 32 keys
+    const bool full = vm == 0xffffffffu;  // every key of the stage is there
     bool ok[2][2];
     float away[2][2];
 #pragma unroll
@@ -286,8 +317,7 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
         const int r = u * 16 + e * 8 + krow;
         ok[u][e] = (vm >> r) & 1u;
         if constexpr (MOD)
-          away[u][e] = static_cast<float>(
-              stripe_pos(k_begin + (warp + i * NW) * KT + r, p, P, a.interleave) - qpos);
+          away[u][e] = static_cast<float>(s_pos[warp][i % NST][r] - qpos);
       }
     uint32_t pb[2][NT][2];  // P^T as the B operand
 #pragma unroll
@@ -302,20 +332,24 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
             x0 = mod_score(sm_mod, x0, slope[n][0], away[u][e]);
             x1 = mod_score(sm_mod, x1, slope[n][1], away[u][e]);
           }
-          x0 = ok[u][e] ? x0 : -INFINITY;
-          x1 = ok[u][e] ? x1 : -INFINITY;
+          if (!full) {
+            x0 = ok[u][e] ? x0 : -INFINITY;
+            x1 = ok[u][e] ? x1 : -INFINITY;
+          }
           st[u][n][2 * e] = x0;
           st[u][n][2 * e + 1] = x1;
           bm0 = fmaxf(bm0, x0);
           bm1 = fmaxf(bm1, x1);
         }
+      // the running max is the same in the lanes of a head and rises only when some key exceeds it by more than 8,
+      // so the maximum over the lanes is needed only then
+      if (__any_sync(0xffffffffu, bm0 > mx[n][0] + 8.f || bm1 > mx[n][1] + 8.f)) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
-        bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
-      }
-      const bool up0 = bm0 > mx[n][0] + 8.f, up1 = bm1 > mx[n][1] + 8.f;
-      if (__any_sync(0xffffffffu, up0 || up1)) {
+        for (int off = 4; off < 32; off <<= 1) {
+          bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
+          bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+        }
+        const bool up0 = bm0 > mx[n][0] + 8.f, up1 = bm1 > mx[n][1] + 8.f;
         const float a0 = up0 ? exp2f(mx[n][0] - bm0) : 1.f;
         const float a1 = up1 ? exp2f(mx[n][1] - bm1) : 1.f;
         if (up0) mx[n][0] = bm0;
@@ -424,7 +458,25 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
     const int d = idx - g * D;
     float out, lse;
     merge_stored<D, G>(sm, NW, g, d, out, lse);
-    if (single) {
+    if (a.fused && single) {
+      const int64_t hq = static_cast<int64_t>(t) * a.num_q_heads + h * G + g;
+      if (a.extra_lse != nullptr) {  // the extra partial merged in
+        const float le = __ldg(a.extra_lse + hq);
+        const float mm = fmaxf(lse, le);
+        if (mm != -INFINITY) {
+          const float e0 = expf(lse - mm), e1 = expf(le - mm);
+          out = (out * e0 + (e1 != 0.f ? e1 * __ldg(a.extra_o + hq * D + d) : 0.f)) / (e0 + e1);
+          lse = mm + logf(e0 + e1);
+        }
+      }
+      if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[hq * D + d] = __float2bfloat16_rn(out);
+      else static_cast<float*>(a.out)[hq * D + d] = out;
+      if (d == 0 && a.lse_out != nullptr) a.lse_out[hq] = lse;
+    } else if (a.fused) {
+      const int64_t wrow = ((static_cast<int64_t>(t) * a.num_kv_heads + h) * a.max_runs + c) * G + g;
+      a.ws_run_o[wrow * D + d] = out;
+      if (d == 0) a.ws_run_lse[wrow] = lse;
+    } else if (single) {
       a.o_part[(orow0 + g) * D + d] = out;
       if (d == 0) a.lse_part[lse_slot(a, p, t, h * G + g)] = lse;
     } else {
@@ -433,25 +485,30 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
       if (d == 0) a.ws_lse[wrow] = lse;
     }
   }
-  if (!single) {
+  if (single) return;
+  if (a.fused) {
+    int32_t* ticket = a.ws_pair + static_cast<int64_t>(t) * a.num_kv_heads + h;
+    if (!take_ticket(ticket, nchunks)) return;
+    merge_runs(a, t, 1, h, nchunks, G, D, sm, CAP);
+    if (threadIdx.x == 0) *ticket = 0;
+  } else {
     if (!take_ticket(a.ws_cnt + slot, nchunks)) return;
     merge_chunks(a, p, h, t, 1, slot, 0, nchunks, G, D, sm, CAP);
     if (threadIdx.x == 0) a.ws_cnt[slot] = 0;
   }
-  if (a.fused) pair_finish(a, t, h, G, D, sm, CAP);
 }
 
 template <int D, int G, bool MOD>
 static int launch_fp4_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   using SM = F4Smem<D>;
   const size_t comb = (static_cast<size_t>(kF4Warps) * G * D + 2 * kF4Warps * G) * sizeof(float);
-  const size_t pages = (static_cast<size_t>(a.chunk) / a.ps_l + 2) * sizeof(int);
+  const size_t pages = (static_cast<size_t>(a.fused ? a.run / a.page_size : a.chunk / a.ps_l) + 2) * sizeof(int);
   const size_t smem = (SM::RING > comb ? SM::RING : comb) + pages;
   auto kern = gqa_partial_fp4_kernel<D, G, MOD>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
-  dim3 grid(a.max_chunks, a.P * a.num_kv_heads, a.qo_indptr != nullptr ? a.num_rows : a.num_tokens);
+  dim3 grid(a.fused ? a.max_runs : a.max_chunks, (a.fused ? 1 : a.P) * a.num_kv_heads, a.qo_indptr != nullptr ? a.num_rows : a.num_tokens);
   *err = launch_pdl(kern, grid, dim3(kF4Warps * 32), smem, s, a);
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

@@ -204,6 +204,20 @@ __device__ __forceinline__ void merge_chunks(const PartialArgs& a, int p, int h,
       scratch, cap);
 }
 
+// Four values of the final output from element oi on (bf16 to nearest even, or fp32).
+__device__ __forceinline__ void store_out4(const PartialArgs& a, int64_t oi, float4 v) {
+  if (a.out_bf16) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+    __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+    uint2 pk;
+    pk.x = *reinterpret_cast<uint32_t*>(&lo);
+    pk.y = *reinterpret_cast<uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + oi) = pk;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + oi) = v;
+  }
+}
+
 // Final output of tokens t0 .. t0 + ntok - 1 for KV head h from the P
 // partner partials (o_part / lse_part rows, which fused calls keep in the
 // workspace) and the optional extra partial (entry P); written as bf16
@@ -226,19 +240,32 @@ __device__ __forceinline__ void merge_partners(const PartialArgs& a, int t0, int
                        : __ldg(a.extra_lse + hq(r));
       },
       [&](int r, int e) { return e < a.P ? a.o_part + (e * pstride + hq(r)) * Dv : a.extra_o + hq(r) * Dv; },
-      [&](int r, int d, float4 v) {
-        const int64_t oi = hq(r) * Dv + d;
-        if (a.out_bf16) {
-          __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
-          __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
-          uint2 pk;
-          pk.x = *reinterpret_cast<uint32_t*>(&lo);
-          pk.y = *reinterpret_cast<uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + oi) = pk;
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + oi) = v;
-        }
+      [&](int r, int d, float4 v) { store_out4(a, hq(r) * Dv + d, v); },
+      [&](int r, float l) {
+        if (a.lse_out != nullptr) a.lse_out[hq(r)] = l;
       },
+      scratch, cap);
+}
+
+// Fused calls whose CTAs take runs of logical pages of every partner: merge the
+// E runs' pieces of tokens t0 .. t0 + ntok - 1 (KV head h) and the optional
+// extra partial into the final output.
+template <int UNR = 1>
+__device__ __forceinline__ void merge_runs(const PartialArgs& a, int t0, int ntok, int h, int E, int Hg, int Dv,
+                                           float* scratch, int cap) {
+  auto hq = [&](int r) -> int64_t {
+    const int i = r / Hg;
+    return static_cast<int64_t>(t0 + i) * a.num_q_heads + h * Hg + (r - i * Hg);
+  };
+  auto wrow = [&](int r, int e) -> int64_t {
+    const int i = r / Hg;
+    return ((static_cast<int64_t>(t0 + i) * a.num_kv_heads + h) * a.max_runs + e) * Hg + (r - i * Hg);
+  };
+  merge_rows<UNR>(
+      ntok * Hg, E + (a.extra_lse != nullptr ? 1 : 0), Dv,
+      [&](int r, int e) { return e < E ? __ldcg(a.ws_run_lse + wrow(r, e)) : __ldg(a.extra_lse + hq(r)); },
+      [&](int r, int e) { return e < E ? a.ws_run_o + wrow(r, e) * Dv : a.extra_o + hq(r) * Dv; },
+      [&](int r, int d, float4 v) { store_out4(a, hq(r) * Dv + d, v); },
       [&](int r, float l) {
         if (a.lse_out != nullptr) a.lse_out[hq(r)] = l;
       },
