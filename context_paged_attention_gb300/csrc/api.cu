@@ -234,6 +234,15 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.max_runs = plan.max_runs;
   a.ws_run_o = ws_part;
   a.ws_run_lse = ws_part_lse;
+  if (f.fused && is_fp8(desc) && modifies(mod)) {
+    // runs of at least the stripe chunk, so that their pieces fit where the
+    // chunks' (or the partners') partials would lie: a row of L keys has
+    // ceil(L / run) of them, and there is room for P * max_chunks >= L / 2048
+    a.run = (4096 + desc->page_size - 1) / desc->page_size * desc->page_size;
+    a.max_runs = max_kv_len > 0 ? (max_kv_len + a.run - 1) / a.run : 1;
+    a.ws_run_o = plan.max_chunks > 1 ? a.ws_o : ws_part;
+    a.ws_run_lse = plan.max_chunks > 1 ? a.ws_lse : ws_part_lse;
+  }
   a.scale = scale;
   a.kv_fp8 = is_fp8(desc);
   a.kv_fp4 = is_fp4(desc);

@@ -125,8 +125,8 @@ struct PartialArgs {
   void* out;               // [T][Hq][Dv], bf16 when out_bf16 else fp32
   int out_bf16;
   float* lse_out;          // [T][Hq] or null
-  // fused calls over E2M1 pools: runs of `run` logical positions (whole pages), every partner's keys of a run
-  // in one CTA; pieces [T * Hkv][max_runs][G][Dv] and their LSEs of rows of several runs
+  // fused decode rows over pools of codes (E2M1; E4M3 with modified scores): runs of `run` logical positions
+  // (whole pages), every partner's keys of a run in one CTA; pieces [T * Hkv][max_runs][G][Dv] and their LSEs
   int run, max_runs;
   float* ws_run_o;
   float* ws_run_lse;
@@ -187,6 +187,8 @@ struct OwnArgs {
 int launch_own_token(const OwnArgs& a, int dtype_bf16, cudaStream_t s, cudaError_t* err);
 int launch_own_token_mma(const OwnArgs& a, cudaStream_t s, cudaError_t* err);  // bf16, tensor cores
 int launch_gqa_partial_mmat(const PartialArgs& a, cudaStream_t s, cudaError_t* err);  // decode rows, groups <= 8
-int launch_gqa_partial_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err);   // decode rows, E2M1 pools
+// decode rows over pools of codes: E2M1, and E4M3 with modified scores
+int launch_gqa_codes_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
+int launch_gqa_codes_e4m3(const PartialArgs& a, cudaStream_t s, cudaError_t* err);
 
 }  // namespace cpattn

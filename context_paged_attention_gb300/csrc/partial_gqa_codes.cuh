@@ -1,34 +1,42 @@
-// cp_paged_attn_partial, GQA rows of one token over an E2M1 (4-bit) pool.
+// GQA rows of one token over pools of codes: E2M1 (4-bit) pools, and E4M3 pools
+// when the scores are modified.
 //
-// A pool row holds D codes of 4 bits (value 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with
-// a sign), an E4M3 scale per 16 values, and the tensor's descale: 72 bytes at
-// D 128 where bf16 takes 256.  The work split, partner addressing and split-KV
-// merge are those of the bf16 decode kernel (CTA = chunk of partner p's stripe
-// of row b for KV head h; stripe slot k at page k / (page_size / P), slot
-// k % (page_size / P) -- mstar PR #1124 "Context / Sequence Parallel 1/5",
-// description).  Fused calls are grouped differently: a CTA takes every
-// partner's keys of a run of logical pages (softmax does not mind the order:
-// partner 0's slots, then partner 1's, ...), so no partner partials are written
-// or merged; a row of one run leaves the CTA as final output, longer rows leave
-// pieces that the row's last CTA merges (run length: fp4_fused_run).
+// An E2M1 row holds D codes of 4 bits (value 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a
+// sign), an E4M3 scale per 16 values, and the tensor's descale: 72 bytes at
+// D 128 where bf16 takes 256 and E4M3 128.  The work split of per-partner calls,
+// the partner addressing and the split-KV merge are those of the bf16 decode
+// kernel (CTA = chunk of partner p's stripe of row b for KV head h; stripe slot k
+// at page k / (page_size / P), slot k % (page_size / P) -- mstar PR #1124
+// "Context / Sequence Parallel 1/5", description).  Fused calls are grouped
+// differently: a CTA takes every partner's keys of a run of logical pages
+// (softmax does not mind the order), so no partner partials are written or
+// merged; a row of one run leaves the CTA as final output, longer rows leave
+// pieces that the row's last CTA merges.
 //
 // Heads on the N side of mma.sync m16n8k16, keys (S^T = K Q^T) and dims
 // (O^T = V^T P^T) on the M side.  The order of the MMA's k index (dims of S,
 // keys of P V) is free as long as both operands follow it, so every lane's
 // codes are consecutive in its row and no ldmatrix is needed:
 //   K: lane (g = lane / 4, q = lane % 4) reads dims [q D/4, (q + 1) D/4) of
-//      keys g and g + 8 with one wide load each; the query fragment follows.
-//   V: the lane reads block g of 16 dims (D 64: half a block) of its four keys
-//      and pairs the codes of two keys by nibble masks, so a byte converts to
-//      the (key, key') operand pair; block g has one scale a key, so the four
-//      scales of a lane serve all of its m-tiles.
-// Codes convert to float16 by cvt (two a instruction) and take their scale in
-// float16: at most 2 + 4 significant bits between 2^-10 and 2688, so the
-// product is exact.  P is rounded to float16 (relative 2^-11 at most, below
+//      keys g and g + 8 with wide loads; the query fragment follows.
+//   V: the lane reads dims [g D/8, (g + 1) D/8) of its four keys and pairs the
+//      codes of two keys (nibble masks, or byte permutes), so a conversion gives
+//      the (key, key') operand pair; at D 128 those are one E2M1 scale block,
+//      whose four scales serve all of the lane's m-tiles.
+// Codes convert to float16 by cvt (two an instruction); E2M1 codes take their
+// scale in float16: at most 2 + 4 significant bits between 2^-10 and 2688, so
+// the product is exact.  P is rounded to float16 (relative 2^-11 at most, below
 // the bf16 output's 2^-9); its sum and the running max stay in float32.
 //
 // Loads: cp.async, 16 bytes a lane for the codes and one row's scales a lane,
-// stages of 32 keys a warp.
+// stages of 32 keys a warp, two in flight.  With modified scores a warp walks
+// its stages from the last key back: scores that fall with the distance then
+// meet their maximum first (front to back raised it, and rescaled O, at almost
+// every stage); otherwise front to back, which is 3% faster.
+// What bounds it: the instructions a key needs (conversion, scale, MMA) more
+// than HBM.
+#pragma once
+
 #include <type_traits>
 
 #include "gqa_core.cuh"
@@ -44,10 +52,10 @@ constexpr int kF4Warps = 4;
 constexpr int kF4Keys = 32;    // keys a stage
 constexpr int kF4Stages = 2;
 
-template <int D>
+template <int D, bool F4>
 struct F4Smem {
-  static constexpr int ROWB = D / 2;        // code bytes of a row
-  static constexpr int SCB = D / 16;        // scale bytes of a row
+  static constexpr int ROWB = F4 ? D / 2 : D;   // code bytes of a row
+  static constexpr int SCB = F4 ? D / 16 : 0;   // scale bytes of a row
   static constexpr int CODES = kF4Keys * ROWB;
   static constexpr int SCALES = kF4Keys * SCB;
   static constexpr int STAGE = 2 * (CODES + SCALES);
@@ -57,10 +65,10 @@ struct F4Smem {
 // stage row of MMA key index r (0..7): the permutation spreads the rows that
 // one phase of the V loads reads over all banks
 __device__ __forceinline__ int f4_row(int r) { return r < 4 ? r : (r ^ 1); }
-// position of 16-byte chunk c of stage row r
-template <int D>
+// position of 16-byte chunk c of stage row r (rows of CH chunks): the same for the K loads' rows
+template <int CH>
 __device__ __forceinline__ int f4_chunk(int c, int r) {
-  return D == 128 ? c ^ (r & 2) : c;
+  return CH == 8 ? c ^ (r & 7) : (CH == 4 ? c ^ (r & 2) : c);
 }
 
 template <int BYTES>
@@ -70,16 +78,18 @@ __device__ __forceinline__ void cp_async_small(void* dst, const void* src) {
 }
 }  // namespace
 
-template <int D, int G, bool MOD>
-__global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_kernel(const PartialArgs a) {
-  using SM = F4Smem<D>;
+// F4: an E2M1 pool, else E4M3.  MOD: modified scores (score_mod.cuh).  E4M3
+// rings take 64 KB, three CTAs an SM.
+template <int D, int G, bool F4, bool MOD>
+__global__ void __launch_bounds__(kF4Warps * 32, G > 8 || !F4 ? 3 : 4) gqa_partial_codes_kernel(const PartialArgs a) {
+  using SM = F4Smem<D, F4>;
   constexpr int NW = kF4Warps, KT = kF4Keys, NST = kF4Stages;
   constexpr int CH = SM::ROWB / 16;        // 16-byte chunks of a row's codes
   constexpr int ITERS = KT * CH / 32;
   constexpr int NT = G > 8 ? 2 : 1;        // n-tiles of 8 heads
   constexpr int MMAS = D / 16;             // k-steps of S^T, m-tiles of O^T
-  constexpr int KW = D / 32;               // code words a lane holds of a key row
-  constexpr int VW = D / 64;               // ... of a value row
+  constexpr int KW = SM::ROWB / 16;        // code words a lane holds of a key row
+  constexpr int VW = SM::ROWB / 32;        // ... of a value row
   constexpr uint32_t NOROW = 0xffffffffu;  // the launch checks that rows fit 32 bits
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_vmask[NW][NST];
@@ -173,16 +183,14 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
   __syncthreads();
   const uint32_t page_rows = static_cast<uint32_t>(a.num_kv_heads) * a.ps_l;
   const uint32_t partner_rows = static_cast<uint32_t>(a.num_pages) * page_rows;
-  // the lane's key of the warp's next stage: slot k of partner p + pp, NW * KT slots further a stage
-  int pp = 0, k = kb + warp * KT + lane, n_pp = stripe_len(L, p, P, a.interleave);
-  auto settle = [&]() {  // k past this partner's slots: on to the next one's
-    while (k >= kb + len && pp < np) {
-      k -= len;
-      ++pp;
-      n_pp = stripe_len(L, p + min(pp, np - 1), P, a.interleave);
-    }
-  };
-  if (nstage > 0) settle();
+  // the lane's key of the warp's next stage: slot k of partner p + pp
+  int pp = 0, k = kb, n_pp = 0;
+  if (my_n > 0) {
+    const int x0 = (warp + (MOD ? (my_n - 1) * NW : 0)) * KT + lane;
+    pp = x0 / len;
+    k = kb + x0 - pp * len;
+    n_pp = stripe_len(L, p + min(pp, np - 1), P, a.interleave);
+  }
 
   // stage i of this warp: lane = key resolves its row and copies its scales,
   // the codes go 32 consecutive chunks an instruction
@@ -197,15 +205,30 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
                   static_cast<uint32_t>(h * a.ps_l + k - j * a.ps_l);
         if constexpr (MOD) s_pos[warp][i % NST][lane] = stripe_pos(k, p + pp, P, a.interleave);
       }
-      k += NW * KT;
-      settle();
+      if constexpr (MOD) {
+        k -= NW * KT;
+        while (k < kb && pp > 0) {
+          k += len;
+          --pp;
+          n_pp = stripe_len(L, p + min(pp, np - 1), P, a.interleave);
+        }
+      } else {
+        k += NW * KT;
+        while (k >= kb + len && pp < np) {
+          k -= len;
+          ++pp;
+          n_pp = stripe_len(L, p + min(pp, np - 1), P, a.interleave);
+        }
+      }
       const uint32_t vm = __ballot_sync(0xffffffffu, myrow != NOROW);
       if (lane == 0) s_vmask[warp][i % NST] = vm;
       uint8_t* sk = ring + (i % NST) * SM::STAGE;
       uint8_t* sv = sk + SM::CODES;
       uint8_t* ssk = sv + SM::CODES + lane * SM::SCB;
       uint8_t* ssv = ssk + SM::SCALES;
-      if (myrow != NOROW) {
+      if constexpr (!F4) {
+        // no scales
+      } else if (myrow != NOROW) {
         cp_async_small<SM::SCB>(ssk, sclk + static_cast<uint64_t>(myrow) * SM::SCB);
         cp_async_small<SM::SCB>(ssv, sclv + static_cast<uint64_t>(myrow) * SM::SCB);
       } else {  // a masked key's value is 0, never NaN
@@ -217,7 +240,7 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
         const int idx = it * 32 + lane;
         const int key = idx / CH, ch = idx - key * CH;
         const uint32_t row = __shfl_sync(0xffffffffu, myrow, key);
-        const int soff = key * SM::ROWB + f4_chunk<D>(ch, key) * 16;
+        const int soff = key * SM::ROWB + f4_chunk<CH>(ch, key) * 16;
         if (row != NOROW) {
           const uint64_t src = static_cast<uint64_t>(row) * SM::ROWB + ch * 16;
           cp_async16(sk + soff, poolk + src);
@@ -276,33 +299,54 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) st[u][n][0] = st[u][n][1] = st[u][n][2] = st[u][n][3] = 0.f;
-      uint32_t kw[2][KW], ks[2][KW / 2];  // keys g8, g8 + 8: code words, one scale a pair of words
+      uint32_t kw[2][KW];  // keys g8, g8 + 8: code words
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = u * 16 + e * 8 + krow;
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sk + r * SM::ROWB + f4_chunk<D>(qi, r) * 16);
-          kw[e][0] = w.x, kw[e][1] = w.y, kw[e][2] = w.z, kw[e][3] = w.w;
-          const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ssk + r * SM::SCB + 2 * qi));
-          ks[e][0] = __byte_perm(s2, 0u, 0x1010u);
-          ks[e][1] = __byte_perm(s2, 0u, 0x3232u);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(sk + r * SM::ROWB + qi * 8);
+        const int row = u * 16 + e * 8 + krow;
+        if constexpr (KW == 2) {
+          const uint2 w = *reinterpret_cast<const uint2*>(sk + row * SM::ROWB + qi * 8);
           kw[e][0] = w.x, kw[e][1] = w.y;
-          ks[e][0] = __byte_perm(e4m3x2_to_f16x2(ssk[r * SM::SCB + qi]), 0u, 0x1010u);
+        } else {
+#pragma unroll
+          for (int x = 0; x < KW / 4; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sk + row * SM::ROWB + f4_chunk<CH>(qi * (KW / 4) + x, row) * 16);
+            kw[e][4 * x] = w.x, kw[e][4 * x + 1] = w.y, kw[e][4 * x + 2] = w.z, kw[e][4 * x + 3] = w.w;
+          }
         }
       }
+      if constexpr (F4) {
+        uint32_t ks[2][KW / 2];  // one scale a pair of words
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
-        const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<0>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
-                                mul_f16x2(e2m1x2_to_f16x2<1>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
-        const uint32_t fb[4] = {mul_f16x2(e2m1x2_to_f16x2<2>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
-                                mul_f16x2(e2m1x2_to_f16x2<3>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
+        for (int e = 0; e < 2; ++e) {
+          const int row = u * 16 + e * 8 + krow;
+          if constexpr (D == 128) {
+            const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ssk + row * SM::SCB + 2 * qi));
+            ks[e][0] = __byte_perm(s2, 0u, 0x1010u);
+            ks[e][1] = __byte_perm(s2, 0u, 0x3232u);
+          } else {
+            ks[e][0] = __byte_perm(e4m3x2_to_f16x2(ssk[row * SM::SCB + qi]), 0u, 0x1010u);
+          }
+        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(st[u][n], fa, qb[n][2 * w][0], qb[n][2 * w][1]);
-          mma_f16(st[u][n], fb, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
+          const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<0>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
+                                  mul_f16x2(e2m1x2_to_f16x2<1>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
+          const uint32_t fb[4] = {mul_f16x2(e2m1x2_to_f16x2<2>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
+                                  mul_f16x2(e2m1x2_to_f16x2<3>(kw[0][w]), s0), mul_f16x2(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(st[u][n], fa, qb[n][2 * w][0], qb[n][2 * w][1]);
+            mma_f16(st[u][n], fb, qb[n][2 * w + 1][0], qb[n][2 * w + 1][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint32_t fa[4] = {e4m3x2_to_f16x2(kw[0][w]), e4m3x2_to_f16x2(kw[1][w]), e4m3x2_to_f16x2(kw[0][w] >> 16),
+                                  e4m3x2_to_f16x2(kw[1][w] >> 16)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(st[u][n], fa, qb[n][w][0], qb[n][w][1]);
         }
       }
     }
@@ -383,36 +427,56 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t vw[4][VW];
-      uint32_t sb[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = u * 16 + (e >> 1) * 8 + ((e & 1) ? vr1 : vr0);
-        if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(sv + r * SM::ROWB + f4_chunk<D>(g8 >> 1, r) * 16 + (g8 & 1) * 8);
+        const int row = u * 16 + (e >> 1) * 8 + ((e & 1) ? vr1 : vr0);
+        const uint8_t* src = sv + row * SM::ROWB + f4_chunk<CH>(g8 * VW / 4, row) * 16 + (g8 * VW * 4) % 16;
+        if constexpr (VW == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src);
+          vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
+        } else if constexpr (VW == 2) {
+          const uint2 w = *reinterpret_cast<const uint2*>(src);
           vw[e][0] = w.x, vw[e][1] = w.y;
-          sb[e] = ssv[r * SM::SCB + g8];
         } else {
-          vw[e][0] = *reinterpret_cast<const uint32_t*>(sv + r * SM::ROWB + g8 * 4);
-          sb[e] = ssv[r * SM::SCB + (g8 >> 1)];
+          vw[e][0] = *reinterpret_cast<const uint32_t*>(src);
         }
       }
-      const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+      if constexpr (F4) {
+        uint32_t sb[4];
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        constexpr uint32_t LO = 0x0f0f0f0fu;
-        const uint32_t e01 = (vw[0][w] & LO) | ((vw[1][w] << 4) & ~LO), o01 = ((vw[0][w] >> 4) & LO) | (vw[1][w] & ~LO);
-        const uint32_t e23 = (vw[2][w] & LO) | ((vw[3][w] << 4) & ~LO), o23 = ((vw[2][w] >> 4) & LO) | (vw[3][w] & ~LO);
-        auto tile = [&](auto ic) {
-          constexpr int x = decltype(ic)::value;
-          const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<x>(e01), s01), mul_f16x2(e2m1x2_to_f16x2<x>(o01), s01),
-                                  mul_f16x2(e2m1x2_to_f16x2<x>(e23), s23), mul_f16x2(e2m1x2_to_f16x2<x>(o23), s23)};
+        for (int e = 0; e < 4; ++e)
+          sb[e] = ssv[(u * 16 + (e >> 1) * 8 + ((e & 1) ? vr1 : vr0)) * SM::SCB + (D == 128 ? g8 : g8 >> 1)];
+        const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * w + x], fa, pb[u][n][0], pb[u][n][1]);
-        };
-        tile(std::integral_constant<int, 0>{});
-        tile(std::integral_constant<int, 1>{});
-        tile(std::integral_constant<int, 2>{});
-        tile(std::integral_constant<int, 3>{});
+        for (int w = 0; w < VW; ++w) {
+          constexpr uint32_t LO = 0x0f0f0f0fu;
+          const uint32_t e01 = (vw[0][w] & LO) | ((vw[1][w] << 4) & ~LO), o01 = ((vw[0][w] >> 4) & LO) | (vw[1][w] & ~LO);
+          const uint32_t e23 = (vw[2][w] & LO) | ((vw[3][w] << 4) & ~LO), o23 = ((vw[2][w] >> 4) & LO) | (vw[3][w] & ~LO);
+          auto tile = [&](auto ic) {
+            constexpr int x = decltype(ic)::value;
+            const uint32_t fa[4] = {mul_f16x2(e2m1x2_to_f16x2<x>(e01), s01), mul_f16x2(e2m1x2_to_f16x2<x>(o01), s01),
+                                    mul_f16x2(e2m1x2_to_f16x2<x>(e23), s23), mul_f16x2(e2m1x2_to_f16x2<x>(o23), s23)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * w + x], fa, pb[u][n][0], pb[u][n][1]);
+          };
+          tile(std::integral_constant<int, 0>{});
+          tile(std::integral_constant<int, 1>{});
+          tile(std::integral_constant<int, 2>{});
+          tile(std::integral_constant<int, 3>{});
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // bytes 2 y, 2 y + 1 of the words: dims 4 w + 2 y, + 1 of the lane's
+            const uint32_t sel = y ? 0x7362u : 0x5140u;
+            const uint32_t p01 = __byte_perm(vw[0][w], vw[1][w], sel), p23 = __byte_perm(vw[2][w], vw[3][w], sel);
+            const uint32_t fa[4] = {e4m3x2_to_f16x2(p01), e4m3x2_to_f16x2(p01 >> 16), e4m3x2_to_f16x2(p23),
+                                    e4m3x2_to_f16x2(p23 >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + y], fa, pb[u][n][0], pb[u][n][1]);
+          }
+        }
       }
     }
   }
@@ -498,13 +562,13 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 ? 3 : 4) gqa_partial_fp4_
   }
 }
 
-template <int D, int G, bool MOD>
-static int launch_fp4_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
-  using SM = F4Smem<D>;
+template <int D, int G, bool F4, bool MOD>
+int launch_codes_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  using SM = F4Smem<D, F4>;
   const size_t comb = (static_cast<size_t>(kF4Warps) * G * D + 2 * kF4Warps * G) * sizeof(float);
   const size_t pages = (static_cast<size_t>(a.fused ? a.run / a.page_size : a.chunk / a.ps_l) + 2) * sizeof(int);
   const size_t smem = (SM::RING > comb ? SM::RING : comb) + pages;
-  auto kern = gqa_partial_fp4_kernel<D, G, MOD>;
+  auto kern = gqa_partial_codes_kernel<D, G, F4, MOD>;
   static std::atomic<int> smem_set[64];
   *err = ensure_smem(kern, smem, smem_set);
   if (*err != cudaSuccess) return CPATTN_ERR_CUDA;
@@ -513,22 +577,22 @@ static int launch_fp4_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) 
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
-template <int D, bool MOD>
-static int fp4_dispatch_g(const PartialArgs& a, int G, cudaStream_t s, cudaError_t* err) {
-  switch (G) {
-    case 1: return launch_fp4_t<D, 1, MOD>(a, s, err);
-    case 2: return launch_fp4_t<D, 2, MOD>(a, s, err);
-    case 4: return launch_fp4_t<D, 4, MOD>(a, s, err);
-    case 8: return launch_fp4_t<D, 8, MOD>(a, s, err);
-    case 16: return launch_fp4_t<D, 16, MOD>(a, s, err);
+template <int D, bool F4, bool MOD>
+int codes_dispatch_g(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch_codes_t<D, 1, F4, MOD>(a, s, err);
+    case 2: return launch_codes_t<D, 2, F4, MOD>(a, s, err);
+    case 4: return launch_codes_t<D, 4, F4, MOD>(a, s, err);
+    case 8: return launch_codes_t<D, 8, F4, MOD>(a, s, err);
+    case 16: return launch_codes_t<D, 16, F4, MOD>(a, s, err);
     default: return CPATTN_ERR_UNSUPPORTED_SHAPE;
   }
 }
 
-int launch_gqa_partial_fp4(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
-  const int G = a.num_q_heads / a.num_kv_heads;
-  if (a.head_dim == 128) return a.has_mod ? fp4_dispatch_g<128, true>(a, G, s, err) : fp4_dispatch_g<128, false>(a, G, s, err);
-  if (a.head_dim == 64) return a.has_mod ? fp4_dispatch_g<64, true>(a, G, s, err) : fp4_dispatch_g<64, false>(a, G, s, err);
+template <bool F4, bool MOD>
+int codes_dispatch(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
+  if (a.head_dim == 128) return codes_dispatch_g<128, F4, MOD>(a, s, err);
+  if (a.head_dim == 64) return codes_dispatch_g<64, F4, MOD>(a, s, err);
   return CPATTN_ERR_UNSUPPORTED_SHAPE;
 }
 

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
 
   auto issue = [&](int i) {
     if (i < my_n) {
-      const int k0 = k_begin + (warp + i * NW) * KT;
+      const int k0 = k_begin + (warp + (MOD ? my_n - 1 - i : i) * NW) * KT;  // MOD: from the last key back
       const int64_t myrow = row_of(k0 + (lane & (KT - 1)));  // lanes 0..15 and 16..31 both cover the 16 keys
       const uint32_t vm = __ballot_sync(0xffffffffu, myrow >= 0) & 0xffffu;
       if (lane == 0) s_vmask[warp][i % NST] = vm;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 2) gqa_partial_mma_kernel(cons
         const bool ok = (vm >> (j * 8 + 2 * qi + e)) & 1u;
         float x0 = (s[j][e] + s_alt[j][e]) * sl, x1 = (s[j][e + 2] + s_alt[j][e + 2]) * sl;
         if constexpr (MOD) {
-          const int k = k_begin + (warp + i * NW) * KT + j * 8 + 2 * qi + e;
+          const int k = k_begin + (warp + (my_n - 1 - i) * NW) * KT + j * 8 + 2 * qi + e;
           const float away = static_cast<float>(stripe_pos(k, p, P, a.interleave) - qpos);
           x0 = mod_score(smod, x0, slope0, away);
           x1 = mod_score(smod, x1, slope1, away);
@@ -478,11 +478,12 @@ int launch_gqa_partial_mma(const PartialArgs& a, cudaStream_t s, cudaError_t* er
   const int G = a.num_q_heads / a.num_kv_heads;
   if (a.head_dim != a.head_dim_v) return CPATTN_ERR_UNSUPPORTED_SHAPE;
   int st = CPATTN_ERR_UNSUPPORTED_SHAPE;
-  // E2M1 pools: the kernel of partial_gqa_fp4.cu; groups of up to 8 heads: the
+  // E2M1 pools, and E4M3 pools with modified scores: partial_gqa_codes.cuh; groups of up to 8 heads: the
   // transposed kernel (partial_gqa_mmat.cu); groups of 16: the head-rows kernel above
-  if (a.kv_fp4) st = launch_gqa_partial_fp4(a, s, err);
+  if (a.kv_fp4) st = launch_gqa_codes_fp4(a, s, err);
+  else if (a.kv_fp8 && a.has_mod) st = launch_gqa_codes_e4m3(a, s, err);
   else if (G <= 8) st = launch_gqa_partial_mmat(a, s, err);
-  else if (G == 16 && a.has_mod) st = a.kv_fp8 ? launch_mma_g16<true, true>(a, s, err) : launch_mma_g16<false, true>(a, s, err);
+  else if (G == 16 && a.has_mod) st = launch_mma_g16<false, true>(a, s, err);
   else if (G == 16) st = a.kv_fp8 ? launch_mma_g16<true, false>(a, s, err) : launch_mma_g16<false, false>(a, s, err);
   // ragged rows may hold several tokens: those rows go to the multi-token kernel
   if (st == CPATTN_OK && a.qo_indptr != nullptr) st = launch_gqa_partial_ext(a, s, err);

@@ -170,7 +170,9 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
   // 0-15 (and 16-31) and shared by shuffle
   auto issue = [&](int i) {
     if (i < my_n) {
-      const int k0 = k_begin + (warp + i * NW) * KT;
+      // modified scores: from the last key back, so that scores that fall with the distance meet their maximum
+      // first (front to back raised it, and rescaled O, at almost every stage)
+      const int k0 = k_begin + (warp + (MOD ? my_n - 1 - i : i) * NW) * KT;
       const int64_t myrow = row_of(k0 + (lane & (KT - 1)));
       const uint32_t vm = __ballot_sync(0xffffffffu, myrow >= 0) & 0xffffu;  // bit k: key k copied
       if (lane == 0) s_vmask[warp][i % NST] = vm;
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
     const bool kb = (vm >> (g8 + 8)) & 1u;  // key g8 + 8
     float v[4];
     if constexpr (MOD) {
-      const int k0 = k_begin + (warp + i * NW) * KT + g8;
+      const int k0 = k_begin + (warp + (my_n - 1 - i) * NW) * KT + g8;
       const float da = static_cast<float>(stripe_pos(k0, p, P, a.interleave) - qpos);
       const float db = static_cast<float>(stripe_pos(k0 + 8, p, P, a.interleave) - qpos);
       v[0] = ka ? mod_score(smod, (st[0] + st2[0]) * sl, slope0, da) : -INFINITY;
@@ -272,10 +274,13 @@ __global__ void __launch_bounds__(kTWarps * 32, F8 ? 4 : 3) gqa_partial_mmat_ker
       v[3] = kb ? (st[3] + st2[3]) * sl : -INFINITY;  // key g8 + 8, head 2 qi + 1
     }
     float bm0 = fmaxf(v[0], v[2]), bm1 = fmaxf(v[1], v[3]);
+    // (MOD: the lanes' maximum only when some lane's rises, as in partial_gqa_codes.cuh)
+    if (!MOD || __any_sync(0xffffffffu, bm0 > m0 + 8.f || bm1 > m1 + 8.f)) {
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
-      bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+      for (int off = 4; off < 32; off <<= 1) {
+        bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, off));
+        bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, off));
+      }
     }
     const bool up0 = bm0 > m0 + 8.f;
     const bool up1 = bm1 > m1 + 8.f;
@@ -455,7 +460,7 @@ static int mmat_dispatch_d(const PartialArgs& a, int G, cudaStream_t s, cudaErro
 // Rows of one token, group size <= 8: the transposed kernel.
 int launch_gqa_partial_mmat(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   const int G = a.num_q_heads / a.num_kv_heads;
-  if (a.has_mod) return a.kv_fp8 ? mmat_dispatch_d<true, true>(a, G, s, err) : mmat_dispatch_d<false, true>(a, G, s, err);
+  if (a.has_mod) return mmat_dispatch_d<false, true>(a, G, s, err);  // E4M3: partial_gqa_codes.cuh
   return a.kv_fp8 ? mmat_dispatch_d<true, false>(a, G, s, err) : mmat_dispatch_d<false, false>(a, G, s, err);
 }
 

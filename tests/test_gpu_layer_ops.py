@@ -3,10 +3,14 @@ float64 oracle.
 
 Attention is checked against the pool's own bytes (decoded by the oracle) and
 the queries the calls took; what the bytes should be is checked apart.  Bars:
-  * P V with probabilities in float16 (one-token rows over 4-bit pools): each is
-    off by 2^-11 relatively, or 2^-25 absolutely below 2^-14, the sum is
-    float32, so |O~ - O| <= 2^-11 A + 2^-25 B with A the weights applied to |V|
-    and B = sum |V| / sum exp(s - max s);
+  * P V with probabilities in float16 (one-token rows over 4-bit pools, and over
+    E4M3 pools with modified scores: the kernel over pools of codes): p~_k = p_k
+    (1 + d_k) + a_k with |d_k| <= 2^-11 and, below 2^-14, |a_k| <= 2^-25 instead;
+    the sum Z of the p_k is float32, so O~ - O = sum (p_k d_k + a_k) v_k / Z and
+    |O~ - O| <= 2^-11 A + 2^-25 sum |v_k| / Z with A the weights applied to |V|.
+    The running max is one of the scores or below the largest, so Z >= sum
+    exp(s - max s) and the second term is at most 2^-25 B, B = sum |V| / sum
+    exp(s - max s);
   * in bf16 (multi-token rows): 2^-8 relatively, normalised by the rounded sum:
     2 * 2^-8 A;
   * in float32 or as a 16-bit pair (the rest): 0;
@@ -66,6 +70,11 @@ def row_values(w, pool, b, n):
     return out
 
 
+def p_float16(w):
+    """Whether one-token rows take the kernel over pools of codes, which rounds P to float16."""
+    return w.kv_dtype == "fp4" or (w.kv_dtype == "fp8" and (w.softcap > 0 or w.slopes is not None))
+
+
 def check_step(w, att, out, lse, heads=None, rows=None):
     """A step's merged output and LSE against the oracle over what the pool holds."""
     K, V = pool_values(att), pool_values(att, True)
@@ -85,7 +94,7 @@ def check_step(w, att, out, lse, heads=None, rows=None):
             if w.dtype == "fp32":
                 bound = 2e-6 * A + 1e-5
             else:
-                pv = 2.0 ** -11 * A + 2.0 ** -25 * Bd if w.decode and w.kv_dtype == "fp4" else 0.0
+                pv = 2.0 ** -11 * A + 2.0 ** -25 * Bd if w.decode and p_float16(w) else 0.0
                 if not w.decode:
                     pv = 2.0 ** -7 * A
                 bound = pv + 1e-4 * A + 2e-5 + 2.0 ** -8 * np.abs(O)
@@ -411,7 +420,7 @@ def test_partials(step):
         for p in range(w.P):
             idx = oracle.stripe_positions(n, w.P, p, w.interleave)
             O, L, A, Bd = oracle.modified_attention(q[t], ks[idx], vs[idx], w.scale, n - 1, idx, w.softcap, w.slopes)
-            pv = 2.0 ** -11 * A + 2.0 ** -25 * Bd if w.kv_dtype == "fp4" else 0.0
+            pv = 2.0 ** -11 * A + 2.0 ** -25 * Bd if p_float16(w) else 0.0
             bound = 2e-6 * A + 1e-5 if w.dtype == "fp32" else pv + 1e-4 * A + 2e-5
             assert_within_bound(att.o_parts[p, t].cpu().numpy(), O, bound, f"O row {b} partner {p}")
             assert_close_lse(att.lse_parts[p, t].cpu().numpy(), L,
