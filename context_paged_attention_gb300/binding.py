@@ -153,7 +153,7 @@ _SIGNATURES = {
 }
 
 
-_Tensor, _int32 = torch.Tensor, torch.int32
+_Tensor, _int32, _float32 = torch.Tensor, torch.int32, torch.float32
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -191,11 +191,9 @@ def _ptr(t):
         return None
     if not isinstance(t, _Tensor):
         raise TypeError("expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("tensor must be contiguous" if t.is_cuda else "tensor must be on a CUDA device")
 
 
 def _i32_tensor(t, what):
@@ -203,7 +201,9 @@ def _i32_tensor(t, what):
         return None
     if t.dtype is not _int32:
         raise TypeError(f"{what} must be int32")
-    return _ptr(t)
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t)  # says what is wrong
 
 
 def _stream(stream):
@@ -231,6 +231,22 @@ def cp_kv_write(desc: PoolDesc, pool_k, pool_v, k_new, v_new, positions, qo_indp
     _check(st, "cp_kv_write")
 
 
+def _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new):
+    """Types and sizes of cp_rope_kv_write's rows (by element counts first: reading five shapes costs
+    as much as the launch)."""
+    dtype, hk = desc.torch_dtype(), desc.num_kv_heads
+    nk, nv, nq = T * hk * desc.head_dim, T * hk * desc.head_dim_v, T * hq * desc.head_dim
+    for name, x, n, heads, d in (("k_new", k_new, nk, hk, desc.head_dim), ("k_out", k_out, nk, hk, desc.head_dim),
+                                 ("v_new", v_new, nv, hk, desc.head_dim_v), ("q", q, nq, hq, desc.head_dim),
+                                 ("q_out", q_out, nq, hq, desc.head_dim)):
+        if x is None:
+            continue
+        if x.dtype is not dtype:
+            raise TypeError(f"{name} must have the layer's dtype {dtype}")
+        if x.numel() != n or x.dim() != 3:
+            raise ValueError(f"{name} must be [{T}, {heads}, {d}]")
+
+
 def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions, qo_indptr, kv_page_indptr,
                      kv_page_indices, cos_sin, q_out, k_out=None, rot_begin=0, style=ROPE_HALVES, dev_status=None,
                      stream=None):
@@ -238,24 +254,15 @@ def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions,
 
     ``cos_sin [positions, rot_dim]`` fp32: ``rot_dim / 2`` cosines, then the sines, a row a position.
     ``q`` and ``q_out`` may both be None (keys only); ``q_out`` may be ``q`` and ``k_out`` ``k_new``."""
-    lib = load_library()
+    lib = _lib or load_library()
     T = positions.numel()
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+    if cos_sin.dim() != 2 or cos_sin.dtype is not _float32:
         raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
-    kv_heads, dtype = desc.num_kv_heads, desc.torch_dtype()
-    shape = (T, kv_heads, desc.head_dim)
-    q_shape = shape if q is None else (T, q.shape[1], desc.head_dim)
-    for name, x, want in (("q", q, q_shape), ("q_out", q_out, q_shape), ("k_new", k_new, shape), ("k_out", k_out, shape),
-                          ("v_new", v_new, (T, kv_heads, desc.head_dim_v))):
-        if x is None:
-            continue
-        if x.dtype is not dtype:
-            raise TypeError(f"{name} must have the layer's dtype {dtype}")
-        if x.shape != want:
-            raise ValueError(f"{name} must be {list(want)}")
+    hq = 0 if q is None else q.shape[1]
+    _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new)
     st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
-                              0 if q is None else q.shape[1], _i32_tensor(positions, "positions"),
-                              _i32_tensor(qo_indptr, "qo_indptr"), qo_indptr.numel() - 1, T,
+                              hq, _i32_tensor(positions, "positions"), _i32_tensor(qo_indptr, "qo_indptr"),
+                              qo_indptr.numel() - 1, T,
                               _i32_tensor(kv_page_indptr, "kv_page_indptr"),
                               _i32_tensor(kv_page_indices, "kv_page_indices"), _ptr(cos_sin), cos_sin.shape[0],
                               int(rot_begin), cos_sin.shape[1], int(style), _ptr(q_out), _ptr(k_out),
@@ -316,7 +323,7 @@ def cp_paged_attn_fused(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_len, k
                         num_rows=None, row_order=None, dev_status=None, stream=None, mod=None):
     """All partners' partials and their merge in one launch (see ``cp_paged_attn_fused`` in cpattn.h);
     ``mod``: modified scores (``score_mod``)."""
-    lib = load_library()
+    lib = _lib or load_library()
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
     dt = DTYPE_BF16 if out.dtype == torch.bfloat16 else DTYPE_FP32
@@ -377,7 +384,7 @@ def own_token_attn(q, k_new, v_new, qo_indptr, num_real_rows, max_q_len, scale, 
     """Causal attention of the step's new tokens (see ``own_token_attn`` in cpattn.h);
     with ``v_new`` None the value width is ``o_own``'s (MLA: the first 512 key values);
     ``mod``: modified scores (``score_mod``; its positions are not used)."""
-    lib = load_library()
+    lib = _lib or load_library()
     T, Hq, D = q.shape
     Hkv = k_new.shape[1]
     Dv = o_own.shape[-1] if v_new is None else v_new.shape[2]

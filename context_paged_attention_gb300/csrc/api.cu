@@ -262,8 +262,10 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.lse_out = f.lse_out;
   a.row_order = f.row_order;
 
-  // tickets start from zero (each call's last arrivals also reset them)
-  if (plan.max_chunks > 1 || f.fused) {
+  // tickets start from zero (each call's last arrivals also reset them); fused calls whose every launch takes whole
+  // page runs use them only for rows of several runs
+  const bool by_runs = f.fused && a.max_runs > 0 && (a.kv_fp4 || a.has_mod);
+  if (by_runs ? a.max_runs > 1 : (plan.max_chunks > 1 || f.fused)) {
     if (cudaMemsetAsync(a.ws_cnt, 0, ticket_bytes, stream) != cudaSuccess) return CPATTN_ERR_CUDA;
   }
   cudaError_t err = cudaSuccess;

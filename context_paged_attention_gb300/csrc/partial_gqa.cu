@@ -248,14 +248,14 @@ size_t PartialPlan::bytes() const {
 
 // Positions of a run of a fused call over an E2M1 pool, in whole pages: one
 // round of CTAs (four an SM) when every row has max_kv_len keys, within
-// [512, 4096].  A CTA's start and end take some 10 us beside its neighbours'
+// [1024, 4096].  A CTA's start and end take some 10 us beside its neighbours'
 // work: 64 rows of 512-8192 keys took 126, 103, 93 and 86 us at runs of 512,
 // 1024, 2048 and 4096 (8 rows of 64k-128k: 458, 312, 246, 227), while few rows
 // need the split to reach every SM.
 static int fp4_fused_run(int page_size, int num_kv_heads, int num_tokens, int max_kv_len) {
   constexpr int kCtas = 4 * 152;
   const int64_t want = (static_cast<int64_t>(num_tokens) * num_kv_heads * max_kv_len + kCtas - 1) / kCtas;
-  const int run = want < 512 ? 512 : (want > 4096 ? 4096 : static_cast<int>(want));
+  const int run = want < 1024 ? 1024 : (want > 4096 ? 4096 : static_cast<int>(want));
   return (run + page_size - 1) / page_size * page_size;
 }
 

@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 || !F4 ? 3 : 4) gqa_parti
   uint8_t* ring = smem + static_cast<size_t>(warp) * NST * SM::STAGE;
   const uint8_t* poolk = static_cast<const uint8_t*>(a.pool_k);
   const uint8_t* poolv = static_cast<const uint8_t*>(a.pool_v);
+  const uint8_t* poolk_lane = poolk + (lane % CH) * 16;  // a lane's chunk of the rows it copies
+  const uint8_t* poolv_lane = poolv + (lane % CH) * 16;
   const uint8_t* sclk = poolk + a.scale_off;
   const uint8_t* sclv = poolv + a.scale_off;
 
@@ -242,9 +244,8 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 || !F4 ? 3 : 4) gqa_parti
         const uint32_t row = __shfl_sync(0xffffffffu, myrow, key);
         const int soff = key * SM::ROWB + f4_chunk<CH>(ch, key) * 16;
         if (row != NOROW) {
-          const uint64_t src = static_cast<uint64_t>(row) * SM::ROWB + ch * 16;
-          cp_async16(sk + soff, poolk + src);
-          cp_async16(sv + soff, poolv + src);
+          cp_async16(sk + soff, poolk_lane + static_cast<uint64_t>(row) * SM::ROWB);
+          cp_async16(sv + soff, poolv_lane + static_cast<uint64_t>(row) * SM::ROWB);
         } else {
           *reinterpret_cast<uint4*>(sv + soff) = make_uint4(0u, 0u, 0u, 0u);
         }

@@ -246,7 +246,7 @@ struct RopeGeo {
 };
 
 template <typename T, int QUANT, int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) rope_pieces_kernel(const RopeArgs a, const RopeGeo geo) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_pieces_kernel(const RopeArgs a, const RopeGeo geo) {
   pdl_trigger();
   pdl_wait();
   const WriteArgs& w = a.w;
@@ -360,7 +360,8 @@ static int launch_pieces(const RopeArgs& a, cudaStream_t s) {
   const dim3 grid((a.w.num_tokens + geo.tokens_per_block - 1) / geo.tokens_per_block,
                   (rows + geo.lanes * ROWS - 1) / (geo.lanes * ROWS));
   if (grid.y > 65535) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  return launch_pdl(rope_pieces_kernel<T, QUANT, ROWS>, grid, dim3(kRopeThreads), 0, s, a, geo) == cudaSuccess
+  const int threads = (geo.tokens_per_block * geo.lanes * geo.units + 31) / 32 * 32;  // no idle warps
+  return launch_pdl(rope_pieces_kernel<T, QUANT, ROWS>, grid, dim3(threads), 0, s, a, geo) == cudaSuccess
              ? CPATTN_OK
              : CPATTN_ERR_CUDA;
 }
