@@ -120,9 +120,12 @@ __global__ void __launch_bounds__(kF4Warps * 32, G > 8 || !F4 ? 3 : 4) gqa_parti
   int nchunks, kb, len, np;
   if (a.fused) {
     nchunks = max(1, (L + a.run - 1) / a.run);
-    const int page0 = c * (a.run / a.page_size);
-    kb = page0 * a.ps_l;
-    len = max(0, min(a.run / a.page_size, (L + a.page_size - 1) / a.page_size - page0)) * a.ps_l;
+    // E2M1: whole runs and a rest (64 rows of 512-8192 keys: 81 us, in equal parts 87); E4M3: equal parts
+    // (8 rows of 16k-64k: 142 us, whole runs 149)
+    const int pages = (L + a.page_size - 1) / a.page_size;
+    const int part = F4 ? a.run / a.page_size : (pages + nchunks - 1) / nchunks;
+    kb = c * part * a.ps_l;
+    len = max(0, min(part, pages - c * part)) * a.ps_l;
     np = P;
   } else {
     const int n_p = stripe_len(L, p, P, a.interleave);
