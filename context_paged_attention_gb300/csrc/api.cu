@@ -159,12 +159,15 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   if (mla && desc->dtype != CPATTN_DTYPE_BF16) return CPATTN_ERR_UNSUPPORTED_SHAPE;
   // E4M3 and E2M1 pools: GQA (the MLA kernel reads bf16 latent rows only)
   if ((is_fp8(desc) || is_fp4(desc) || modifies(mod)) && mla) return CPATTN_ERR_UNSUPPORTED_SHAPE;
-  // the E2M1 decode kernel keeps pool rows as 32-bit values (2^32 - 1 rows are 137 GB of codes at D 64)
-  if (is_fp4(desc) && pool_rows(desc) >= 0xffffffffLL) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  // the decode kernel over codes keeps pool rows as 32-bit values (2^32 - 1 rows are 137 GB of E2M1 codes at D 64)
+  if ((is_fp4(desc) || (is_fp8(desc) && modifies(mod))) && pool_rows(desc) >= 0xffffffffLL)
+    return CPATTN_ERR_UNSUPPORTED_SHAPE;
   // multi-token rows over a pool of 16-bit or narrower rows: the kernel's copy warps pass pool row
   // indices as 32-bit values (checked here, before the one-token rows' launch)
-  if (!mla && qo_indptr != nullptr && !is_fp8(desc) && pool_rows(desc) >= (int64_t{1} << 31))
+  if (!mla && qo_indptr != nullptr && (!is_fp8(desc) || modifies(mod)) && pool_rows(desc) >= (int64_t{1} << 31))
     return CPATTN_ERR_UNSUPPORTED_SHAPE;
+  // run and stripe lengths are rounded up in 32 bits
+  if ((is_fp4(desc) || modifies(mod)) && max_kv_len > (1 << 30)) return CPATTN_ERR_UNSUPPORTED_SHAPE;
 
   PartialPlan plan;
   if (!plan_partial(mla, f.fused, is_fp4(desc), desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads, num_q_heads,
@@ -262,9 +265,9 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.lse_out = f.lse_out;
   a.row_order = f.row_order;
 
-  // tickets start from zero (each call's last arrivals also reset them); fused calls whose every launch takes whole
-  // page runs use them only for rows of several runs
-  const bool by_runs = f.fused && a.max_runs > 0 && (a.kv_fp4 || a.has_mod);
+  // tickets start from zero (each call's last arrivals also reset them); fused decode calls that take whole page runs
+  // use them only for rows of several runs
+  const bool by_runs = f.fused && qo_indptr == nullptr && a.max_runs > 0 && (a.kv_fp4 || a.has_mod);
   if (by_runs ? a.max_runs > 1 : (plan.max_chunks > 1 || f.fused)) {
     if (cudaMemsetAsync(a.ws_cnt, 0, ticket_bytes, stream) != cudaSuccess) return CPATTN_ERR_CUDA;
   }

@@ -14,9 +14,13 @@
 //
 // Fused calls: one CTA takes all P partners' keys of a run of logical pages
 // (softmax does not mind the order: partner 0's slots, then partner 1's, ...),
-// so no partner partials leave the SM; a row of more than one run leaves
-// normalised pieces in the workspace, merged by a second kernel.  Per-partner
-// calls: one CTA takes a chunk of one partner's stripe.
+// so no partner partials leave the SM; items (a block of a row's tokens and a
+// head) of more than one run leave normalised pieces in the workspace, merged
+// by a second kernel.  Batches of more items than about one a SM are cut
+// differently: the cost of all items (from the lengths on the device, so a
+// captured call stays balanced) is divided into equal parts, one a CTA, that
+// takes whole items and at most two cut ones.  Per-partner calls: one CTA takes
+// a chunk of one partner's stripe.
 //
 // Roles: warps 0-3 and 4-7 own tiles 0 and 1 (thread = query row = TMEM lane:
 // online softmax, running max raised only when it grows by more than 8 in log2
@@ -65,6 +69,7 @@ constexpr int kUnit = 32;       // keys of a tile that one copy warp takes
 constexpr int kUnits = kTile / kUnit;
 constexpr int kThreads = 32 * (kLoadWarp + 2 * kUnits);
 constexpr int kRun = 2048;      // logical positions of a fused CTA's page run, at least
+constexpr int kSms = 152;
 constexpr int kMergeUnroll = 4;
 
 // barriers (arrival counts in brackets)
@@ -102,12 +107,83 @@ struct Layout {
 // FMT of the pool
 constexpr int kBf16 = 0, kE4m3 = 1, kFp4 = 2;
 
+// Cost of a page for a block with two query tiles or one (a tile's softmax and
+// MMAs overlap the other's), and the positions whose time an item's start and
+// end take.
+constexpr int kCost2 = 5, kCost1 = 3, kStart = 640;
+
+// Where a CTA is in its equal part: row b has ntok tokens from tok0 on and
+// `pages` pages; its item (head h, block blk) begins at cost `start`, the CTA
+// goes on from page pg0 of it up to cost `end`.  In shared memory between items.
+// Piece c of nchunks of the item is pages [pg0, pg1).
+struct Place {
+  long long start, end, per;
+  int b, h, tok0, ntok, pages, blk, pg0, pg1, c, nchunks;
+};
+
+// What the walk over rows, heads and blocks needs to know.
+struct Walk {
+  const int32_t* qo_indptr;
+  const int32_t* kv_len;
+  int num_rows, num_kv_heads, max_kv_len, page_size, start, qt;
+
+  __device__ bool row(Place& w, int r) const {  // false: the row has fewer than two tokens
+    if (r >= num_rows) return false;
+    w.b = r;
+    w.tok0 = __ldg(qo_indptr + r);
+    w.ntok = __ldg(qo_indptr + r + 1) - w.tok0;
+    if (w.ntok < 2) return false;
+    const long long L = min(__ldg(kv_len + r), max_kv_len);
+    w.pages = max(1, static_cast<int>((L + page_size - 1) / page_size));
+    return true;
+  }
+  __device__ int page_cost(const Place& w, int blk) const { return w.ntok - blk * 2 * qt > qt ? kCost2 : kCost1; }
+  __device__ long long item_cost(const Place& w, int blk) const {
+    return start + static_cast<long long>(w.pages) * page_cost(w, blk);
+  }
+  __device__ int last_blk(const Place& w) const { return (w.ntok - 1) / (2 * qt); }
+  __device__ long long head_cost(const Place& w) const {
+    return last_blk(w) * (start + static_cast<long long>(w.pages) * kCost2) + item_cost(w, last_blk(w));
+  }
+  // The pages of the item that this CTA takes, from pg0 on; false: its part
+  // ends before the next one.  A part's border inside an item lies at the page
+  // it falls into, so an item's pieces go from the part that reaches the end
+  // of its first page to the one that holds its last unit.
+  __device__ bool span(Place& w) const {
+    const int cost = page_cost(w, w.blk);
+    const long long left = w.end - w.start - start;
+    w.pg1 = left < cost ? 0 : static_cast<int>(min(static_cast<long long>(w.pages), left / cost));
+    const long long first = (w.start + start + cost - 1) / w.per;
+    w.c = static_cast<int>(blockIdx.x - first);
+    w.nchunks = static_cast<int>((w.start + item_cost(w, w.blk) - 1) / w.per - first) + 1;
+    return w.pg1 > w.pg0;
+  }
+};
+
+// The current item (or run), for its output: piece c of nchunks of head h's
+// tokens [s0, s1).
+struct Item {
+  int c, nchunks, h, s0, s1, ntiles;
+};
+
+// E2M1 pools keep a CTA a run: in the loop over items their copy warps, which
+// bound that kernel, lose more than the equal parts give (269 us for 253).
+__host__ __device__ constexpr bool can_even(int fmt) { return fmt != kFp4; }
+
 struct Geo {
   int run;          // fused: logical positions of a CTA's page run (whole pages)
-  int max_runs;     // grid.x
-  float* ws_o;      // fused, several runs: [T * Hkv][max_runs][G][D]
+  int max_runs;     // pieces a row can have (grid.x of a CTA a run)
+  int64_t least;    // fused, equal parts: least cost of a part (0: a CTA a run)
+  int start;        // cost of an item beside its pages
+  float* ws_o;      // fused, several pieces: [T * Hkv][max_runs][G][D]
   float* ws_lse;    // [T * Hkv][max_runs][G]
 };
+
+// A value the compiler cannot carry from one loop iteration to the next.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
 
 // 16-bit pair of a P row, and the MMA's operand type
 template <bool F16>
@@ -198,6 +274,93 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, const
   }
   return false;
 }
+// The start of this CTA's part; false: it has no page.  (Called, like
+// next_place, rather than inlined: the registers of their 64-bit divisions do
+// not belong beside the roles' loops.)
+static __device__ __noinline__ bool first_place(const Walk walk, int64_t least, Place& place, long long* s_part) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place w;
+  long long mine = 0;
+  for (int r = tid; r < walk.num_rows; r += kThreads)
+    if (walk.row(w, r)) mine += walk.head_cost(w);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_part[warp] = mine;
+  if (tid == 0) place.b = -1;
+  __syncthreads();
+  long long total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) total += s_part[i];
+  total *= walk.num_kv_heads;
+  const long long per = max(static_cast<long long>(least), (total + gridDim.x - 1) / gridDim.x);
+  const long long x = blockIdx.x * per;
+  if (x >= total) return false;
+  // the row that cost x falls into
+  long long before = 0;
+  for (int r0 = 0; r0 < walk.num_rows; r0 += kThreads) {
+    const long long u = walk.row(w, r0 + tid) ? walk.head_cost(w) * walk.num_kv_heads : 0;
+    long long incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) s_part[warp] = incl;
+    __syncthreads();
+    long long lo = before + incl - u;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) lo += s_part[i];
+      before += s_part[i];
+    }
+    if (u > 0 && x >= lo && x < lo + u) {
+      long long rel = x - lo;
+      w.h = static_cast<int>(rel / walk.head_cost(w));
+      rel -= w.h * walk.head_cost(w);
+      const long long item = walk.start + static_cast<long long>(w.pages) * kCost2;
+      w.blk = static_cast<int>(min(rel / item, static_cast<long long>(walk.last_blk(w))));
+      rel -= w.blk * item;
+      w.per = per;
+      w.end = min(x + per, total);
+      w.start = x - rel;
+      w.pg0 = rel > walk.start ? static_cast<int>((rel - walk.start) / walk.page_cost(w, w.blk)) : 0;
+      if (!walk.span(w)) w.b = -1;
+      place = w;
+    }
+    __syncthreads();
+    if (place.b >= 0 || before > x) break;
+  }
+  return place.b >= 0;
+}
+
+// On to the next block, head or row; false: the part ends.
+static __device__ __noinline__ bool next_place(const Walk walk, Place& place, int* s_scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place w = place;
+  w.start += walk.item_cost(w, w.blk);
+  w.pg0 = 0;
+  bool more = w.start < w.end;
+  if (more && w.blk++ == walk.last_blk(w)) {
+    w.blk = 0;
+    if (++w.h == walk.num_kv_heads) {
+      w.h = 0;
+      const int r1 = w.b + 1;
+      int next = walk.num_rows;
+      for (int r0 = r1; r0 < walk.num_rows && next == walk.num_rows; r0 += kThreads) {
+        const unsigned has = __ballot_sync(0xffffffffu, walk.row(w, r0 + tid));
+        if (lane == 0) s_scan[warp] = has ? r0 + warp * 32 + __ffs(has) - 1 : walk.num_rows;
+        __syncthreads();
+        for (int i = 0; i < kThreads / 32; ++i) next = min(next, s_scan[i]);
+        __syncthreads();
+      }
+      more = walk.row(w, next);
+    }
+  }
+  more = more && walk.span(w);
+  __syncthreads();
+  if (tid == 0) place = w;
+  __syncthreads();
+  return more;
+}
 }  // namespace pieces
 
 template <int D, int G, int FMT, bool MOD>
@@ -212,26 +375,25 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_scan[kThreads / 32];
   __shared__ int s_row[3];  // row, first token, end token of this CTA's block
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sK = base + Lt::OFF_K;
-  uint8_t* sV = base + Lt::OFF_V;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Lt::OFF_BAR);
-  uint32_t* smask = reinterpret_cast<uint32_t*>(base + Lt::OFF_MASK);  // [slot][unit]: keys with data
-  float* spos = reinterpret_cast<float*>(base + Lt::OFF_POS);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + Lt::OFF_MISC);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(base + Lt::OFF_MISC + 4);
-  int* spg = reinterpret_cast<int*>(base + Lt::OFF_PG);
-  auto bar = [&](int i) { return tc05::smem_addr(&bars[i]); };
+  __shared__ long long s_part[kThreads / 32];
+  __shared__ Place s_place;
+  __shared__ Item s_item;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: roles branch without divergence
-  const int P = a.P, c = blockIdx.x, z = blockIdx.z;
+  const bool even = can_even(FMT) && geo.least > 0;  // equal parts of all rows; else a CTA a run (or a chunk of a stripe)
+  const int P = a.P, z = blockIdx.z;
+  int c = blockIdx.x;
   const int p0 = a.fused ? 0 : blockIdx.y / a.num_kv_heads;
-  const int h = blockIdx.y - p0 * a.num_kv_heads;
+  int h = blockIdx.y - p0 * a.num_kv_heads;
   const int t_real = __ldg(a.qo_indptr + a.num_rows);
 
   // ---- block z of padding tokens past the last row: 0 / -inf (chunk 0's CTAs)
-  if (c == 0) {
+  if (even) {
+    const int64_t n = static_cast<int64_t>(max(0, a.num_tokens - t_real)) * a.num_kv_heads;
+    for (int64_t x = blockIdx.x; x < n; x += gridDim.x)
+      fused_zero_token(a, t_real + static_cast<int>(x / a.num_kv_heads), static_cast<int>(x % a.num_kv_heads), G, D);
+  } else if (c == 0) {
     const int lo = t_real + z * QB, hi = min(lo + QB, a.num_tokens);
     for (int tok = lo; tok < hi; ++tok) {
       if (a.fused) {
@@ -245,8 +407,12 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   }
   // ---- row block z: rows of >= 2 tokens in order, ceil(n / QB) blocks each (one-token rows are the
   // decode kernel's), found with a block-wide prefix sum over the rows
-  if (tid == 0) s_row[0] = -1;
-  {
+  int b = -1, s0 = 0, s1 = 0;
+  const Walk walk = {a.qo_indptr, a.kv_len, a.num_rows, a.num_kv_heads, a.max_kv_len, a.page_size, geo.start, QT};
+  if (even) {
+    if (!first_place(walk, geo.least, s_place, s_part)) return;
+  } else {
+    if (tid == 0) s_row[0] = -1;
     int done_blocks = 0;
     for (int r0 = 0; r0 < a.num_rows; r0 += blockDim.x) {
       const int r = r0 + tid;
@@ -279,10 +445,35 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       done_blocks = total;
     }
     __syncthreads();
+    b = s_row[0];
+    if (b < 0) return;
+    s0 = s_row[1];
+    s1 = s_row[2];
   }
-  const int b = s_row[0];
-  if (b < 0) return;
-  const int s0 = s_row[1], s1 = s_row[2];
+  bool tmem = false;
+  // equal parts: every item of this CTA's part in turn
+#pragma unroll 1
+  for (;;) {
+  // what an item derives from these is computed again for the next: kept across items it would cost the roles' loops
+  // registers that they do not have
+  const int tid = opaque(threadIdx.x), lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: roles branch without divergence
+  uint8_t* base = smem_raw + opaque(static_cast<int>((1024u - (tc05::smem_addr(smem_raw) & 1023u)) & 1023u));
+  uint8_t* sK = base + Lt::OFF_K;
+  uint8_t* sV = base + Lt::OFF_V;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Lt::OFF_BAR);
+  uint32_t* smask = reinterpret_cast<uint32_t*>(base + Lt::OFF_MASK);  // [slot][unit]: keys with data
+  float* spos = reinterpret_cast<float*>(base + Lt::OFF_POS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + Lt::OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(base + Lt::OFF_MISC + 4);
+  int* spg = reinterpret_cast<int*>(base + Lt::OFF_PG);
+  auto bar = [&](int i) { return tc05::smem_addr(&bars[i]); };
+  if (even) {
+    b = s_place.b;
+    h = s_place.h;
+    s0 = s_place.tok0 + s_place.blk * QB;
+    s1 = s_place.tok0 + min(s_place.ntok, s_place.blk * QB + QB);
+  }
   int L = __ldg(a.kv_len + b);
   if (L > a.max_kv_len) {
     if (c == 0 && tid == 0) report(a.dev_status, CPATTN_DEV_POS_PAST_TABLE);
@@ -290,13 +481,20 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   }
   // ---- this CTA's keys: stripe slots [kb, kb + len) of partners p0 .. p0 + np - 1
   int nchunks, kb, len, np;
-  if (a.fused) {
+  if (even) {
+    c = s_place.c;
+    nchunks = s_place.nchunks;
+    kb = s_place.pg0 * a.ps_l;
+    len = max(0, static_cast<int>(min(static_cast<long long>(s_place.pg1 - s_place.pg0) * a.ps_l,
+                                      static_cast<long long>(stripe_len(L, 0, P, a.interleave)) - kb)));
+    np = P;
+  } else if (a.fused) {
     nchunks = max(1, (L + geo.run - 1) / geo.run);
-    // equal parts (16 rows of 2-256 tokens on up to 8192 E2M1 keys: 255 us; whole runs and a rest 264)
-    const int pages = (L + a.page_size - 1) / a.page_size;
-    const int part = (pages + nchunks - 1) / nchunks;
+    // equal runs (16 rows of 2-256 tokens on up to 8192 E2M1 keys: 255 us; whole runs and a rest 264)
+    const int n = (L + a.page_size - 1) / a.page_size;
+    const int part = (n + nchunks - 1) / nchunks;
     kb = c * part * a.ps_l;
-    len = max(0, min(part, pages - c * part)) * a.ps_l;
+    len = max(0, min(part, n - c * part)) * a.ps_l;
     np = P;
   } else {
     const int n_p = stripe_len(L, p0, P, a.interleave);
@@ -307,7 +505,8 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   }
   if (c >= nchunks) return;
   const int ntiles = (np * len + kTile - 1) / kTile;
-  const bool single = nchunks == 1;
+  if (tid == 0) s_item = Item{c, nchunks, h, s0, s1, ntiles};
+  __syncthreads();
   const int ntl = s1 - s0 > QT ? 2 : 1;          // query tiles with tokens
   const int my_t = warp >> 2;                    // softmax threads: tile, row, token, head
   const int my_r = (warp & 3) * 32 + lane;
@@ -317,7 +516,6 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
 
   float l = 0.f, m = -INFINITY;  // softmax rows: sum and running max (log2)
   bool alive = true;
-  uint32_t tbase = 0;
   if (ntiles > 0) {
     // ---- page ids of the CTA's slots, checked once
     const int j0 = kb / a.ps_l;
@@ -346,16 +544,18 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
         if (i < B_KFREE || (i >= B_VFULL && i < B_VFREE)) cnt = F16 ? kUnits : 32 * kUnits;
         if (i >= B_PFULL && i < B_PVDONE) cnt = 4;
         if (i == B_Q) cnt = 4 * ntl;
+        if (tmem) tc05::mbar_inval(bar(i));  // every phase of the last item's is over
         tc05::mbar_init(bar(i), cnt);
       }
       *s_abort = 0;
       tc05::mbar_init_fence();
     }
-    if (warp == 0) tc05::tmem_alloc(tc05::smem_addr(tmem_slot), Lt::TMEM_COLS);
+    if (warp == 0 && !tmem) tc05::tmem_alloc(tc05::smem_addr(tmem_slot), Lt::TMEM_COLS);
+    tmem = true;
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
-    tbase = *tmem_slot;
+    const uint32_t tbase = *tmem_slot;
 
     if (warp >= kLoadWarp) {
       // ================= copies =================
@@ -540,6 +740,8 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
           }
           if (++st == kKStages) st = 0, ph ^= 1;
         }
+        for (int j = max(0, ntiles - kKStages); j < ntiles && alive; ++j)
+          alive = wait_phase(bar0 + 8 * (B_KFREE + j % kKStages), (j / kKStages) & 1, s_abort);
       } else {
         constexpr uint32_t id_o = F16 ? tc05::idesc_f16(128, D, false, true) : tc05::idesc_bf16(128, D, false, true);
         const uint64_t dv0 = tc05::desc_mn128(tc05::smem_addr(sV), Lt::BLK);
@@ -568,6 +770,8 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
           }
           if (++st == kVStages) st = 0, ph ^= 1;
         }
+        for (int j = max(0, ntiles - kVStages); j < ntiles && alive; ++j)
+          alive = wait_phase(bar0 + 8 * (B_VFREE + j % kVStages), (j / kVStages) & 1, s_abort);
       }
       if (!alive) {
         *s_abort = 1;
@@ -716,15 +920,30 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
         if (lane == 0) ws_arrive(bar(B_PFULL + 2 * my_t + bb));
       }
       if (alive) {
-        const int last = ntiles - 1;
-        const bool ok = wait_phase(bar(B_PVDONE + 2 * my_t + (last & 1)), (last >> 1) & 1, s_abort);
+        bool ok = true;
+        for (int i = max(0, ntiles - 2); i < ntiles; ++i)
+          ok = ok && wait_phase(bar(B_PVDONE + 2 * my_t + (i & 1)), (i >> 1) & 1, s_abort);
         alive = __all_sync(0xffffffffu, ok);
       }
       if (!alive) *s_abort = 1;
     }
   }
 
-  // ---- softmax rows: output, or a normalised piece with its LSE
+  // ---- softmax rows: output, or a normalised piece with its LSE.  (What the item's loops need not know is read, or
+  // computed, again.)
+  {
+  const Item it = s_item;
+  const int c = it.c, nchunks = it.nchunks, h = it.h, s0 = it.s0, s1 = it.s1, ntiles = it.ntiles;
+  const int tid = opaque(threadIdx.x), lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t tbase = ntiles > 0 ? *tmem_slot : 0u;
+  const bool single = nchunks == 1;
+  const int ntl = s1 - s0 > QT ? 2 : 1;
+  const int my_t = warp >> 2;
+  const int my_r = (warp & 3) * 32 + lane;
+  const int my_tok = s0 + my_t * QT + my_r / G;
+  const int my_g = my_r % G;
+  const bool my_ok = warp < kSoftWarps && my_tok < s1;
   if (warp < kSoftWarps && my_t < ntl && alive) {
     tc05::fence_after_sync();
     const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -750,6 +969,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       const int64_t wrow = ((static_cast<int64_t>(my_tok) * a.num_kv_heads + h) * geo.max_runs + c) * G + my_g;
       dst = geo.ws_o + wrow * D;
       ldst = geo.ws_lse + wrow;
+      if (my_ok && my_g == 0 && c == nchunks - 1) a.ws_pair[static_cast<int64_t>(my_tok) * a.num_kv_heads + h] = nchunks;
     } else if (single) {
       dst = a.o_part + ((static_cast<int64_t>(p0) * a.num_tokens) * a.num_q_heads + hq) * D;
       ldst = a.lse_part + lse_slot(a, p0, my_tok, h * G + my_g);
@@ -822,23 +1042,22 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
     tc05::bulk_wait_all();
     if (my_ok && ldst != nullptr) *ldst = lse_all;
   }
-  if (ntiles > 0) {
-    tc05::fence_before_sync();
-    __syncthreads();
-    const bool ok_all = *s_abort == 0;
-    if (warp == 0) tc05::tmem_dealloc(tbase, Lt::TMEM_COLS);
-    if (!ok_all) {
-      if (tid == 0) report(a.dev_status, CPATTN_DEV_TC_TIMEOUT);
-      return;
-    }
-  }
-  if (single || a.fused) return;  // fused rows of several runs: gqa_pieces_merge_kernel
+  tc05::fence_before_sync();
+  __syncthreads();
+  const bool failed = ntiles > 0 && *s_abort != 0;
+  if (failed && tid == 0) report(a.dev_status, CPATTN_DEV_TC_TIMEOUT);
+  if (even && !failed && next_place(walk, s_place, s_scan)) continue;
+  if (tmem && warp == 0) tc05::tmem_dealloc(tbase, Lt::TMEM_COLS);
+  if (failed || single || a.fused) return;  // fused rows of several pieces: gqa_pieces_merge_kernel
   // ---- per-partner calls: the stripe's last CTA merges its chunks
   const int64_t slot0 = (static_cast<int64_t>(s0) * P + p0) * a.num_kv_heads + h;
   if (!take_ticket(a.ws_cnt + slot0, nchunks)) return;
   merge_chunks<kMergeUnroll>(a, p0, h, s0, s1 - s0, slot0, static_cast<int64_t>(P) * a.num_kv_heads, nchunks, G, D,
                              reinterpret_cast<float*>(base), Lt::SCRATCH);
   if (tid == 0) a.ws_cnt[slot0] = 0;
+  return;
+  }
+  }
 }
 
 // Fused calls: the exact merge of a row's pieces and the extra partial, a block
@@ -858,11 +1077,9 @@ __global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialA
   const int t = blockIdx.x;
   const int b = find_row_warp(a.qo_indptr, a.num_rows, t);
   if (b < 0 || __ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b) < 2) return;  // one-token rows: the decode kernel's
-  const int L = min(__ldg(a.kv_len + b), a.max_kv_len);
-  const int E = (L + geo.run - 1) / geo.run;
-  if (E < 2) return;
   const int part = lane / LN, c4 = lane - part * LN;
   for (int h0 = warp * NH; h0 < a.num_q_heads; h0 += (blockDim.x >> 5) * NH) {
+    int E[NH], most = 0;      // pieces (0: the item's only CTA wrote its output)
     int64_t w0[NH], row[NH];  // piece e of head i: workspace row w0 + e G
     float le[NH], mx[NH], sum[NH];
     float4 acc[NH], vx[NH];
@@ -870,15 +1087,19 @@ __global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialA
     for (int i = 0; i < NH; ++i) {
       const int hq = min(h0 + i, a.num_q_heads - 1);  // past the last head: its work again, not written
       row[i] = static_cast<int64_t>(t) * a.num_q_heads + hq;
-      w0[i] = (static_cast<int64_t>(t) * a.num_kv_heads + hq / G) * geo.max_runs * G + hq % G;
+      const int64_t item = static_cast<int64_t>(t) * a.num_kv_heads + hq / G;
+      E[i] = __ldg(a.ws_pair + item);
+      most = max(most, E[i]);
+      w0[i] = item * geo.max_runs * G + hq % G;
       le[i] = a.extra_lse != nullptr ? __ldg(a.extra_lse + row[i]) : -INFINITY;
       vx[i] = acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       sum[i] = 0.f;
     }
+    if (most == 0) continue;
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       mx[i] = le[i];
-      for (int e = lane; e < E; e += 32) mx[i] = fmaxf(mx[i], __ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e) * G));
+      for (int e = lane; e < E[i]; e += 32) mx[i] = fmaxf(mx[i], __ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e) * G));
       if (le[i] != -INFINITY) vx[i] = __ldg(reinterpret_cast<const float4*>(a.extra_o + row[i] * D) + c4);
     }
 #pragma unroll
@@ -887,14 +1108,14 @@ __global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialA
       for (int o = 16; o > 0; o >>= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
       if (mx[i] == -INFINITY) mx[i] = 0.f;  // no keys anywhere: every weight 0
     }
-    for (int e0 = 0; e0 < E; e0 += 32) {
+    for (int e0 = 0; e0 < most; e0 += 32) {
       float we[NH];
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
-        we[i] = e0 + lane < E ? expf(__ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e0 + lane) * G) - mx[i]) : 0.f;
+        we[i] = e0 + lane < E[i] ? expf(__ldg(geo.ws_lse + w0[i] + static_cast<int64_t>(e0 + lane) * G) - mx[i]) : 0.f;
         sum[i] += we[i];
       }
-      const int n = min(32, E - e0);
+      const int n = min(32, most - e0);
 #pragma unroll 2
       for (int eb = 0; eb < n; eb += PARTS) {
         const int e = eb + part;
@@ -928,7 +1149,7 @@ __global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialA
       acc[i].z = fmaf(wx, vx[i].z, acc[i].z);
       acc[i].w = fmaf(wx, vx[i].w, acc[i].w);
       sum[i] += wx;
-      if (h0 + i >= a.num_q_heads) continue;
+      if (h0 + i >= a.num_q_heads || E[i] == 0) continue;
       const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
       if (part == 0) {
         const int64_t oi = row[i] * D + c4 * 4;
@@ -954,6 +1175,18 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
     geo.run = (kRun + a.page_size - 1) / a.page_size * a.page_size;
     geo.max_runs = a.max_kv_len > 0 ? (a.max_kv_len + geo.run - 1) / geo.run : 1;
     page_slots = geo.run / a.page_size + 1;
+    // A CTA a run where that is about one round of CTAs.  Else all rows' pages
+    // in equal parts, one a CTA, as long as a part's page ids fit: whole items
+    // need no merge, and every SM ends at the same time (16 rows of 2-256
+    // tokens on up to 8192 bf16 keys, both modifications: 290 us for 301).
+    const int64_t pages = (static_cast<int64_t>(a.max_kv_len) + a.page_size - 1) / a.page_size;
+    const int64_t ctas = static_cast<int64_t>(geo.max_runs) * a.num_kv_heads * ((a.num_tokens + QB - 1) / QB);
+    const int64_t room = static_cast<int64_t>(a.P) * a.max_chunks;  // pieces a row and head
+    if (can_even(FMT) && ctas > kSms && room > 1 && Layout<D>::smem_bytes(0) + 4 * (pages + 1) <= 227 * 1024) {
+      geo.least = (pages * kCost2 + room - 2) / (room - 1);
+      geo.start = (kStart * kCost2 + a.page_size - 1) / a.page_size;
+      page_slots = static_cast<int>(pages) + 1;
+    }
     // The pieces lie where the per-partner kernels keep theirs (this launch
     // starts when theirs are done).  A row of L keys has ceil(L / run) runs,
     // and run >= 2048, the stripe chunk: stripes of more than one chunk have
@@ -961,7 +1194,8 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
     // ones for P >= L / 2048.
     geo.ws_o = a.max_chunks > 1 ? a.ws_o : a.o_part;
     geo.ws_lse = a.max_chunks > 1 ? a.ws_lse : a.lse_part;
-    if (geo.max_runs > a.P * a.max_chunks) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+    if (geo.max_runs > room) return CPATTN_ERR_UNSUPPORTED_SHAPE;
+    if (geo.least > 0) geo.max_runs = static_cast<int>(room);
   } else {
     geo.max_runs = a.max_chunks;
     page_slots = a.chunk / a.ps_l + 2;
@@ -978,7 +1212,7 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   // row blocks: at most one partial block a row beyond T / QB full ones (the
   // first T / QB of them also cover the blocks of padding tokens)
   const int qblocks = (a.num_tokens + QB - 1) / QB;
-  dim3 grid(geo.max_runs, (a.fused ? 1 : a.P) * a.num_kv_heads, a.num_rows + qblocks);
+  const dim3 grid = geo.least > 0 ? dim3(kSms) : dim3(geo.max_runs, (a.fused ? 1 : a.P) * a.num_kv_heads, a.num_rows + qblocks);
   kern<<<grid, kThreads, smem, s>>>(a, geo);
   *err = cudaGetLastError();
   if (*err == cudaSuccess && a.fused && geo.max_runs > 1) {

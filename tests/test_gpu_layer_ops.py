@@ -373,6 +373,11 @@ STEPS = {
     "mixed_fp4": lambda: W.scored(F4(_mixed(64, 16, 1, 128, 2, 8, new=(5, 1, 20), ctx=(300, 20, 0))), 2.0, SLOPES(16)),
     "mixed_fp32": lambda: W.scored(_mixed(65, 4, 2, 64, 2, 8, dtype="fp32", new=(1, 9), ctx=(300, 15)), 2.0, SLOPES(4)),
     "mixed_split": lambda: W.scored(_mixed(66, 4, 1, 128, 1, 16, new=(5, 1), ctx=(2500, 2100)), 0.0, SLOPES(4)),
+    # more blocks of tokens than SMs: pieces in equal parts, several items a CTA, cut and whole ones
+    "mixed_many": lambda: W.scored(_spread(_mixed(67, 32, 2, 64, 4, 16, new=(1, 300, 2, 17, 1, 250, 16, 33),
+                                                  ctx=(900, 2500, 2500, 0, 3, 1100, 40, 700)), 4.0), 20.0, SLOPES(32)),
+    "mixed_many_e4m3": lambda: W.scored(F8(_mixed(68, 32, 4, 128, 2, 32, I=2, new=(290, 1, 2, 33, 250, 64),
+                                                  ctx=(2100, 700, 2049, 5, 1, 333))), 0.0, SLOPES(32)),
     # as a layer runs them: rotation on the way in, 4-bit pool, modified scores
     "layer_decode": lambda: W.scored(F4(W.rotated(_decode(70, 8, 2, 128, 4, 16, [700, 0, 33]), 128)), 30.0, SLOPES(8)),
     "layer_mixed": lambda: W.scored(F4(W.rotated(_mixed(71, 8, 2, 128, 4, 16), 64, 64, pairs=True)), 30.0, SLOPES(8)),
