@@ -213,6 +213,13 @@ def _stream(stream):
     return _current_raw_stream(_current_device())
 
 
+def _here(*tensors):
+    """The calls launch on the current device: tensors of another one are refused."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != _current_device():
+            raise ValueError(f"tensors must be on the current CUDA device ({_current_device()})")
+
+
 def _check(status, what):
     if status != 0:
         raise CpattnError(status, what)
@@ -222,6 +229,8 @@ def cp_kv_write(desc: PoolDesc, pool_k, pool_v, k_new, v_new, positions, qo_indp
                 kv_page_indices, dev_status=None, stream=None):
     """Write new K/V rows into the striped pool (see ``cp_kv_write`` in cpattn.h)."""
     lib = load_library()
+    if desc.fp4:
+        _here(pool_k, k_new)
     num_rows = qo_indptr.numel() - 1
     st = lib.cp_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(k_new), _ptr(v_new),
                          _i32_tensor(positions, "positions"), _i32_tensor(qo_indptr, "qo_indptr"), num_rows,
@@ -259,6 +268,7 @@ def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions,
     if cos_sin.dim() != 2 or cos_sin.dtype is not _float32:
         raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
     hq = 0 if q is None else q.shape[1]
+    _here(pool_k, k_new, positions)
     _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new)
     st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
                               hq, _i32_tensor(positions, "positions"), _i32_tensor(qo_indptr, "qo_indptr"),
@@ -286,6 +296,7 @@ def _mod(mod, heads, tokens):
     if mod is None:
         return None
     slopes, positions = mod.tensors
+    _here(slopes, positions)
     if slopes is not None and slopes.numel() != heads:
         raise ValueError(f"slopes must have one value for each of the {heads} query heads")
     if positions is not None and positions.numel() != tokens:
@@ -324,6 +335,8 @@ def cp_paged_attn_fused(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_len, k
     """All partners' partials and their merge in one launch (see ``cp_paged_attn_fused`` in cpattn.h);
     ``mod``: modified scores (``score_mod``)."""
     lib = _lib or load_library()
+    if mod is not None or desc.fp4:
+        _here(pool_k, q, out)
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
     dt = DTYPE_BF16 if out.dtype == torch.bfloat16 else DTYPE_FP32
@@ -344,6 +357,8 @@ def cp_paged_attn_partial_ex(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_l
     """cp_paged_attn_partial with the LSE layout chosen (see ``cp_paged_attn_partial_ex`` in cpattn.h);
     ``mod``: modified scores (``score_mod``)."""
     lib = load_library()
+    if mod is not None or desc.fp4:
+        _here(pool_k, q, o_part)
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
     st = lib.cp_paged_attn_partial_mod(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
@@ -385,6 +400,8 @@ def own_token_attn(q, k_new, v_new, qo_indptr, num_real_rows, max_q_len, scale, 
     with ``v_new`` None the value width is ``o_own``'s (MLA: the first 512 key values);
     ``mod``: modified scores (``score_mod``; its positions are not used)."""
     lib = _lib or load_library()
+    if mod is not None:
+        _here(q, k_new, o_own)
     T, Hq, D = q.shape
     Hkv = k_new.shape[1]
     Dv = o_own.shape[-1] if v_new is None else v_new.shape[2]

@@ -114,10 +114,5 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// float16 pair -> bf16 pair (nearest even; exact for at most 8 significant bits).
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_bf16(f.x, f.y);
-}
 
 }  // namespace cpattn

@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
       const int x0 = unit * kUnit + lane;
       int pp = ((ntiles - 1) * kTile + x0) / len, k = kb + (ntiles - 1) * kTile + x0 - pp * len;
       int n_pp = stripe_len(L, p0 + min(pp, np - 1), P, a.interleave);
-      // pool row of the lane's key of the next tile (-1: no key), its position; advances the key
+      // pool row of the lane's key of the next tile (-1: no key), its position counted from the row's end (exact in
+      // float32 where it matters however long the row); advances the key
       auto next_row = [&](float& pos) -> int {
         int row = -1;
         if (pp < np && k < n_pp) {
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
           if (pg >= 0)
             row = static_cast<int>(((static_cast<int64_t>(p0 + pp) * a.num_pages + pg) * a.num_kv_heads + h) * a.ps_l +
                                    (k - j * a.ps_l));
-          if (MOD && is_k) pos = static_cast<float>(stripe_pos(k, p0 + pp, P, a.interleave));
+          if (MOD && is_k) pos = static_cast<float>(stripe_pos(k, p0 + pp, P, a.interleave) - L);
         }
         k -= kTile;
         while (k < kb && pp > 0) {
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
         smod = score_mod_of(a.softcap, kscale);
         if (a.slopes != nullptr && my_ok) {
           slope2 = __ldg(a.slopes + h * G + my_g) * kLog2e;
-          qpos = static_cast<float>(query_pos(a, b, my_tok, __ldg(a.qo_indptr + b)));
+          qpos = static_cast<float>(query_pos(a, b, my_tok, __ldg(a.qo_indptr + b)) - L);
         }
       }
       {  // this thread's query row, in the MMA layout (and type)

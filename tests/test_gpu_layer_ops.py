@@ -516,6 +516,74 @@ def test_extreme_scores():
         check_step(wl, att, att.out, att.lse)
 
 
+def test_workspace_contents_do_not_matter(step):
+    w, att = step
+    for run in (att.run_step, att.run_step_fused):
+        a = [x.clone() for x in run()]
+        for ws in (att.workspace, att._fused_ws):
+            if ws is not None:
+                ws.fill_(0xFF)
+        b = run()
+        torch.cuda.synchronize()
+        assert att.status() == 0
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_calls_at_once():
+    """Steps of different shapes on two streams, each with its own workspace."""
+    atts = [_att(STEPS[n]()) for n in ("mixed_many", "fp4_split", "mixed_fp4", "both_e4m3")]
+    want = [[x.clone() for x in att.run_step_fused()] for att in atts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in atts]
+    for att in atts:
+        att.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for att, s in zip(atts, streams):
+            att.run_step_fused(s)
+    torch.cuda.synchronize()
+    for att, (o, l_) in zip(atts, want):
+        assert att.status() == 0 and torch.equal(att.out, o) and torch.equal(att.lse, l_)
+
+
+@pytest.mark.parametrize("name", ["mixed_many", "mixed_many_e4m3", "fp4_split", "mixed_fp4", "split"])
+def test_replay_with_other_lengths(name):
+    """Work is split by the lengths on the device: a captured step follows them."""
+    w = STEPS[name]()
+    att = _att(w)
+    att.capture(fused=True)
+    full = att.kv_len.clone()
+    for lens in (full // 2, full * 0 + 1, full * 0, full):
+        att.kv_len.copy_(torch.minimum(lens.clamp(min=1) if w.decode else lens, full))
+        o, l_ = (x.clone() for x in att.replay())
+        torch.cuda.synchronize()
+        assert att.status() == 0
+        a = [x.clone() for x in att.run_step_fused()]
+        b = att.run_step()
+        torch.cuda.synchronize()
+        assert torch.equal(o, a[0]) and torch.equal(l_, a[1])
+        n = int(w.qo_indptr[w.num_real_rows])
+        # each path is within 2^-7 of the largest value's size of the definition
+        torch.testing.assert_close(o[:n].float(), b[0][:n].float(), rtol=2 ** -6, atol=2 ** -6 * float(b[0][:n].abs().max()))
+
+
+def test_other_device_is_refused(monkeypatch):
+    from context_paged_attention_gb300 import binding as B
+
+    atts = [_att(STEPS[n]()) for n in ("layer_plain", "fp4_g8", "cap_bf16", "mixed")]
+    for att in atts:
+        att.run_step()
+        att.run_step_fused()
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream()
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    for att in atts:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            att.run_step(stream)
+        with pytest.raises(ValueError, match="current CUDA device"):
+            att.run_step_fused(stream)
+
+
 def test_other_stream_and_full_size_sample():
     """The full-size 4-bit decode batch on a side stream, sampled rows."""
     w = W.rotated(W.gqa_decode_fp4(batch=64), 128)
