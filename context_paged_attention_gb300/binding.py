@@ -153,7 +153,7 @@ _SIGNATURES = {
 }
 
 
-_Tensor, _int32, _float32 = torch.Tensor, torch.int32, torch.float32
+_int32, _float32 = torch.int32, torch.float32
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -189,10 +189,11 @@ def version() -> int:
 def _ptr(t):
     if t is None:
         return None
-    if not isinstance(t, _Tensor):
-        raise TypeError("expected a torch.Tensor")
-    if t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
     raise ValueError("tensor must be contiguous" if t.is_cuda else "tensor must be on a CUDA device")
 
 
@@ -243,17 +244,15 @@ def cp_kv_write(desc: PoolDesc, pool_k, pool_v, k_new, v_new, positions, qo_indp
 def _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new):
     """Types and sizes of cp_rope_kv_write's rows (by element counts first: reading five shapes costs
     as much as the launch)."""
-    dtype, hk = desc.torch_dtype(), desc.num_kv_heads
-    nk, nv, nq = T * hk * desc.head_dim, T * hk * desc.head_dim_v, T * hq * desc.head_dim
-    for name, x, n, heads, d in (("k_new", k_new, nk, hk, desc.head_dim), ("k_out", k_out, nk, hk, desc.head_dim),
-                                 ("v_new", v_new, nv, hk, desc.head_dim_v), ("q", q, nq, hq, desc.head_dim),
-                                 ("q_out", q_out, nq, hq, desc.head_dim)):
+    dtype, hk, d, dv = desc.torch_dtype(), desc.num_kv_heads, desc.head_dim, desc.head_dim_v
+    for name, x, heads, n in (("k_new", k_new, hk, d), ("k_out", k_out, hk, d), ("v_new", v_new, hk, dv),
+                              ("q", q, hq, d), ("q_out", q_out, hq, d)):
         if x is None:
             continue
         if x.dtype is not dtype:
             raise TypeError(f"{name} must have the layer's dtype {dtype}")
-        if x.numel() != n or x.dim() != 3:
-            raise ValueError(f"{name} must be [{T}, {heads}, {d}]")
+        if x.numel() != T * heads * n or x.dim() != 3:
+            raise ValueError(f"{name} must be [{T}, {heads}, {n}]")
 
 
 def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions, qo_indptr, kv_page_indptr,
@@ -267,15 +266,15 @@ def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions,
     T = positions.numel()
     if cos_sin.dim() != 2 or cos_sin.dtype is not _float32:
         raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
-    hq = 0 if q is None else q.shape[1]
-    _here(pool_k, k_new, positions)
+    hq = 0 if q is None else q.size(1)
+    _here(pool_k, k_new)
     _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new)
     st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
                               hq, _i32_tensor(positions, "positions"), _i32_tensor(qo_indptr, "qo_indptr"),
                               qo_indptr.numel() - 1, T,
                               _i32_tensor(kv_page_indptr, "kv_page_indptr"),
-                              _i32_tensor(kv_page_indices, "kv_page_indices"), _ptr(cos_sin), cos_sin.shape[0],
-                              int(rot_begin), cos_sin.shape[1], int(style), _ptr(q_out), _ptr(k_out),
+                              _i32_tensor(kv_page_indices, "kv_page_indices"), _ptr(cos_sin), cos_sin.size(0),
+                              int(rot_begin), cos_sin.size(1), int(style), _ptr(q_out), _ptr(k_out),
                               _i32_tensor(dev_status, "dev_status"), _stream(stream))
     _check(st, "cp_rope_kv_write")
 
@@ -336,8 +335,8 @@ def cp_paged_attn_fused(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_len, k
     ``mod``: modified scores (``score_mod``)."""
     lib = _lib or load_library()
     if mod is not None or desc.fp4:
-        _here(pool_k, q, out)
-    T, Hq = q.shape[0], q.shape[1]
+        _here(pool_k, q)
+    T, Hq = q.size(0), q.size(1)
     B = kv_len.numel() if num_rows is None else num_rows
     dt = DTYPE_BF16 if out.dtype == torch.bfloat16 else DTYPE_FP32
     st = lib.cp_paged_attn_fused_mod(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
@@ -358,7 +357,7 @@ def cp_paged_attn_partial_ex(desc: PoolDesc, pool_k, pool_v, q, kv_len, max_kv_l
     ``mod``: modified scores (``score_mod``)."""
     lib = load_library()
     if mod is not None or desc.fp4:
-        _here(pool_k, q, o_part)
+        _here(pool_k, q)
     T, Hq = q.shape[0], q.shape[1]
     B = kv_len.numel() if num_rows is None else num_rows
     st = lib.cp_paged_attn_partial_mod(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), Hq, B, T,
@@ -401,7 +400,7 @@ def own_token_attn(q, k_new, v_new, qo_indptr, num_real_rows, max_q_len, scale, 
     ``mod``: modified scores (``score_mod``; its positions are not used)."""
     lib = _lib or load_library()
     if mod is not None:
-        _here(q, k_new, o_own)
+        _here(q)
     T, Hq, D = q.shape
     Hkv = k_new.shape[1]
     Dv = o_own.shape[-1] if v_new is None else v_new.shape[2]
