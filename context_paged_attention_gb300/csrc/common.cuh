@@ -92,18 +92,6 @@ __device__ __forceinline__ int find_row(const int32_t* __restrict__ indptr, int 
   return lo;
 }
 
-// The same by a whole warp, 32 row ends a step (two dependent loads fewer than
-// a binary search of 32 rows takes); -1 when t is past the last row.
-__device__ __forceinline__ int find_row_warp(const int32_t* __restrict__ indptr, int num_rows, int t) {
-  const int lane = threadIdx.x & 31;
-  for (int r0 = 0; r0 < num_rows; r0 += 32) {
-    const int r = r0 + lane;
-    const unsigned hit = __ballot_sync(0xffffffffu, r < num_rows && __ldg(indptr + r + 1) > t);
-    if (hit != 0u) return r0 + __ffs(hit) - 1;
-  }
-  return -1;
-}
-
 // 2^x by the hardware approximation (PTX ex2.approx.ftz.f32: relative error
 // about 2^-22, results below 2^-126 flushed to zero).  Used where the
 // probability is rounded to bf16 right after (relative step 2^-9).

@@ -12,7 +12,8 @@
 // for 256 rows, and while the tensor core works for one tile the softmax warps
 // of the other keep the exponential and issue slots busy.
 //
-// Fused calls: one CTA takes all P partners' keys of a run of logical pages
+// Fused calls: one CTA takes all P partners' keys of a run of logical pages,
+// 2048 or 4096 positions
 // (softmax does not mind the order: partner 0's slots, then partner 1's, ...),
 // so no partner partials leave the SM; items (a block of a row's tokens and a
 // head) of more than one run leave normalised pieces in the workspace, merged
@@ -68,9 +69,10 @@ constexpr int kLoadWarp = 10;   // K: 10, 11, V: 12, 13
 constexpr int kUnit = 32;       // keys of a tile that one copy warp takes
 constexpr int kUnits = kTile / kUnit;
 constexpr int kThreads = 32 * (kLoadWarp + 2 * kUnits);
-constexpr int kRun = 2048;      // logical positions of a fused CTA's page run, at least
+constexpr int kRun = 2048;      // logical positions of a fused CTA's page run, or twice as many
 constexpr int kSms = 152;
 constexpr int kMergeUnroll = 4;
+constexpr int kMergeWarps = 4;
 
 // barriers (arrival counts in brackets)
 constexpr int B_KFULL = 0;                    // [64 lanes (cp.async) or 2 warps] x4
@@ -1061,26 +1063,27 @@ __global__ void __launch_bounds__(pieces::kThreads, 1) gqa_pieces_kernel(const P
   }
 }
 
-// Fused calls: the exact merge of a row's pieces and the extra partial, a block
-// a token and a warp two of its heads at a time.  Its own kernel, because a
+// Fused calls: the exact merge of an item's pieces and the extra partial, a
+// block eight heads of a token and a warp two of them.  Its own kernel, because a
 // block's last CTA alone took 34 us for the 256 rows of its merge (a row of E
 // pieces is E + 1 short reads, which one SM cannot keep enough of in flight).
-// What it spends is the chain of dependent small reads (row, length, LSEs,
-// values), so blocks are many and light: four heads a warp at 128 registers
-// took 35 us for 2064 tokens.
+// What it spends is the chain of dependent small reads (number of pieces, LSEs,
+// values), so blocks are many and light: about 25 us for 2064 tokens of 32
+// heads; four heads a warp at 128 registers took 35.
 template <int D>
-__global__ void __launch_bounds__(256, 5) gqa_pieces_merge_kernel(const PartialArgs a, const pieces::Geo geo, int G) {
+__global__ void __launch_bounds__(32 * pieces::kMergeWarps, 8)
+    gqa_pieces_merge_kernel(const PartialArgs a, const pieces::Geo geo, int G) {
   pdl_wait();
+  using pieces::kMergeWarps;
   constexpr int NH = 2;            // heads a warp merges together
   constexpr int LN = D / 4;        // lanes a row takes
   constexpr int PARTS = 32 / LN;   // pieces read at once
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x;
-  const int b = find_row_warp(a.qo_indptr, a.num_rows, t);
-  if (b < 0 || __ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b) < 2) return;  // one-token rows: the decode kernel's
   const int part = lane / LN, c4 = lane - part * LN;
-  for (int h0 = warp * NH; h0 < a.num_q_heads; h0 += (blockDim.x >> 5) * NH) {
-    int E[NH], most = 0;      // pieces (0: the item's only CTA wrote its output)
+  for (int h0 = (blockIdx.y * kMergeWarps + warp) * NH; h0 < a.num_q_heads; h0 += gridDim.y * kMergeWarps * NH) {
+    int E[NH], most = 0;      // pieces (0: the item's only CTA wrote its output, or the token's row has no other
+                              // token: its ticket here is 0 again)
     int64_t w0[NH], row[NH];  // piece e of head i: workspace row w0 + e G
     float le[NH], mx[NH], sum[NH];
     float4 acc[NH], vx[NH];
@@ -1173,24 +1176,33 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   Geo geo = {};
   int page_slots;
   if (a.fused) {
-    geo.run = (kRun + a.page_size - 1) / a.page_size * a.page_size;
-    geo.max_runs = a.max_kv_len > 0 ? (a.max_kv_len + geo.run - 1) / geo.run : 1;
+    const int64_t room = static_cast<int64_t>(a.P) * a.max_chunks;  // pieces a row and head
+    const int64_t blocks = static_cast<int64_t>(a.num_kv_heads) * ((a.num_tokens + QB - 1) / QB);
+    auto runs = [&](int positions) {
+      geo.run = (positions + a.page_size - 1) / a.page_size * a.page_size;
+      geo.max_runs = a.max_kv_len > 0 ? (a.max_kv_len + geo.run - 1) / geo.run : 1;
+    };
+    // Longer runs where there are CTAs enough all the same: half the pieces to
+    // merge (16 rows of 2-256 tokens on up to 8192 E2M1 keys: 243 us, runs of
+    // 2048 250, of 8192 272).
+    runs(kRun);
+    if (geo.max_runs * blocks > 4 * kSms) runs(2 * kRun);
     page_slots = geo.run / a.page_size + 1;
     // A CTA a run where that is about one round of CTAs.  Else all rows' pages
     // in equal parts, one a CTA, as long as a part's page ids fit: whole items
     // need no merge, and every SM ends at the same time (16 rows of 2-256
     // tokens on up to 8192 bf16 keys, both modifications: 290 us for 301).
     const int64_t pages = (static_cast<int64_t>(a.max_kv_len) + a.page_size - 1) / a.page_size;
-    const int64_t ctas = static_cast<int64_t>(geo.max_runs) * a.num_kv_heads * ((a.num_tokens + QB - 1) / QB);
-    const int64_t room = static_cast<int64_t>(a.P) * a.max_chunks;  // pieces a row and head
-    if (can_even(FMT) && ctas > kSms && room > 1 && Layout<D>::smem_bytes(0) + 4 * (pages + 1) <= 227 * 1024) {
+    if (can_even(FMT) && geo.max_runs * blocks > kSms && room > 1 &&
+        Layout<D>::smem_bytes(0) + 4 * (pages + 1) <= 227 * 1024) {
       geo.least = (pages * kCost2 + room - 2) / (room - 1);
       geo.start = (kStart * kCost2 + a.page_size - 1) / a.page_size;
       page_slots = static_cast<int>(pages) + 1;
     }
     // The pieces lie where the per-partner kernels keep theirs (this launch
     // starts when theirs are done).  A row of L keys has ceil(L / run) runs,
-    // and run >= 2048, the stripe chunk: stripes of more than one chunk have
+    // and run >= 2048, the stripe chunk (equal parts are as long as the room
+    // needs): stripes of more than one chunk have
     // room for P * max_chunks >= L / 2048 pieces a row and head, shorter
     // ones for P >= L / 2048.
     geo.ws_o = a.max_chunks > 1 ? a.ws_o : a.o_part;
@@ -1217,7 +1229,7 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   kern<<<grid, kThreads, smem, s>>>(a, geo);
   *err = cudaGetLastError();
   if (*err == cudaSuccess && a.fused && geo.max_runs > 1) {
-    *err = launch_pdl(gqa_pieces_merge_kernel<D>, dim3(a.num_tokens), dim3(256), 0, s, a, geo, G);
+    *err = launch_pdl(gqa_pieces_merge_kernel<D>, dim3(a.num_tokens, (a.num_q_heads + 2 * kMergeWarps - 1) / (2 * kMergeWarps)), dim3(32 * kMergeWarps), 0, s, a, geo, G);
   }
   return *err == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

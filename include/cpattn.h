@@ -244,11 +244,15 @@ CPATTN_API int cp_rope_kv_write(const cpattn_pool_desc* desc, void* pool_k, void
  *   lse_part   [P][num_tokens][num_q_heads] fp32
  *   workspace  device scratch of cp_paged_attn_workspace_bytes(...) bytes, or
  *              more; its contents need no initialisation and are clobbered.
+ *              One call at a time: calls, or replays of captured graphs, that
+ *              may run at once need a workspace each.
  * Supported: GQA with head_dim in {64, 128}, group size in {1, 2, 4, 8, 16};
  * MLA (num_kv_heads 1, head_dim 576, head_dim_v 512, bf16, 128 query heads).
- * Other shapes, and multi-token rows over a bf16 pool of 2^31 or more K rows
- * (P * num_pages * num_kv_heads * page_size / P), return
- * CPATTN_ERR_UNSUPPORTED_SHAPE before any launch.
+ * Other shapes, multi-token rows over a pool of 2^31 or more K rows
+ * (P * num_pages * num_kv_heads * page_size / P), E2M1 pools of 2^32 - 1 or
+ * more, and max_kv_len above 2^30 with an E2M1 pool or modified scores return
+ * CPATTN_ERR_UNSUPPORTED_SHAPE (all but unmodified multi-token rows over E4M3
+ * pools before any launch).
  */
 CPATTN_API int cp_paged_attn_partial(const cpattn_pool_desc* desc, const void* pool_k,
                           const void* pool_v, const void* q, int32_t num_q_heads,
@@ -335,7 +339,10 @@ CPATTN_API int cp_paged_attn_partial_mod(const cpattn_pool_desc* desc, const voi
  * _forward_with_dcp: merge_attn_states of the context and query partials).
  * Here the merge is fused into the partial kernels.  GQA heads: every chunk
  * of every partner leaves its partial in the workspace and the last CTA of
- * each (token, KV head) merges them.  MLA over pages of 64 slots: one tile
+ * each (token, KV head) merges them; over E2M1 pools, and where scores are
+ * modified over E4M3 pools or for multi-token rows, a CTA takes every
+ * partner's keys of a run of logical pages instead, so that rows of one run
+ * are written as they are and only longer ones leave pieces.  MLA over pages of 64 slots: one tile
  * holds a logical page of every partner, so the online softmax merges the
  * partners as it goes and the kernel writes final rows; a token whose pages
  * are split between two CTA pairs leaves normalised pieces in the workspace,
