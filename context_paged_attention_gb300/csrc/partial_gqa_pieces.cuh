@@ -13,11 +13,10 @@
 // of the other keep the exponential and issue slots busy.
 //
 // Fused calls: one CTA takes all P partners' keys of a run of logical pages,
-// 2048 or 4096 positions
-// (softmax does not mind the order: partner 0's slots, then partner 1's, ...),
-// so no partner partials leave the SM; items (a block of a row's tokens and a
-// head) of more than one run leave normalised pieces in the workspace, merged
-// by a second kernel.  Batches of more items than about one a SM are cut
+// 2048 or 4096 positions (softmax does not mind the order: partner 0's slots,
+// then partner 1's, ...), so no partner partials leave the SM; items (a block
+// of a row's tokens and a head) of more than one run leave normalised pieces in
+// the workspace, merged by a second kernel.  Batches of more items than about one a SM are cut
 // differently: the cost of all items (from the lengths on the device, so a
 // captured call stays balanced) is divided into equal parts, one a CTA, that
 // takes whole items and at most two cut ones.  Per-partner calls: one CTA takes
