@@ -502,6 +502,70 @@ def test_rejected_pages_leave_their_keys_out():
                 assert_close_lse(att.lse_parts[p, t].cpu().numpy(), L, 2e-4, kind)
 
 
+SHORT_TABLES = {
+    "fp4": lambda: F4(_decode(90, 8, 2, 128, 4, 16, [63, 700, 31])),
+    "e4m3_scored": lambda: W.scored(F8(_decode(91, 8, 2, 128, 4, 16, [63, 700, 31])), 20.0, SLOPES(8)),
+    "fp4_mixed": lambda: F4(_mixed(92, 8, 2, 128, 4, 16, new=(4, 40), ctx=(60, 300))),
+    "mixed_scored": lambda: W.scored(_mixed(93, 8, 2, 128, 4, 16, new=(4, 40), ctx=(60, 300)), 20.0, SLOPES(8)),
+    "mixed_many": lambda: W.scored(_mixed(94, 32, 2, 64, 4, 16, new=(4, 300, 300, 33), ctx=(60, 2500, 2400, 700)), 0.0,
+                                   SLOPES(32)),
+}
+
+
+@pytest.mark.parametrize("name", sorted(SHORT_TABLES))
+def test_table_shorter_than_the_length(name):
+    """Keys past a row's page table are left out and reported; the next row's pages are not read for them."""
+    w = SHORT_TABLES[name]()
+    att = _att(w)
+    att.max_kv_len = max(att.max_kv_len, 200)
+    from context_paged_attention_gb300 import binding as B
+
+    att.workspace = torch.empty(B.workspace_bytes(att.desc, w.num_q_heads, w.num_tokens, att.max_kv_len),
+                                dtype=torch.uint8, device="cuda")
+    att.kv_len[0] = 64  # the first row's four pages, full
+    for run in (att.run_step, att.run_step_fused):
+        want = [x.clone() for x in run()]
+        torch.cuda.synchronize()
+        assert att.status() == 0
+        att.kv_len[0] = 64 + 75
+        got = [x.clone() for x in run()]
+        torch.cuda.synchronize()
+        assert att.status() == 2
+        att.dev_status.zero_()
+        att.kv_len[0] = 64
+        n = int(w.qo_indptr[w.num_real_rows])
+        top = float(want[0][:n].abs().max())
+        # the split may differ with the lengths: two results of one definition
+        torch.testing.assert_close(got[0][:n].float(), want[0][:n].float(), rtol=0, atol=2 ** -6 * top)
+        torch.testing.assert_close(got[1][:n], want[1][:n], rtol=0, atol=2e-4 + 2 ** -19 * float(want[1][:n].abs().max()))
+
+
+def test_partials_without_a_workspace():
+    """The call with the library's own scratch takes 4-bit pools too, split stripes among them."""
+    import ctypes
+
+    from context_paged_attention_gb300 import binding as B
+
+    lib = ctypes.CDLL(B.library_path())
+    fn, vp, i32 = lib.cp_paged_attn_partial_noalloc, ctypes.c_void_p, ctypes.c_int32
+    fn.argtypes = [ctypes.POINTER(B.PoolDesc), vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, ctypes.c_float, vp, vp,
+                   vp, vp]
+    for name in ("fp4_split", "fp4_mixed_g1_split"):
+        w = STEPS[name]()
+        att = _att(w)
+        att.run_step()
+        o, l_ = torch.full_like(att.o_parts[:w.P], 7.0), torch.full_like(att.lse_parts[:w.P], 7.0)
+        st = fn(ctypes.byref(att.desc), att.pool_k.data_ptr(), att.pool_v.data_ptr(), att.q.data_ptr(), w.num_q_heads,
+                w.num_rows, w.num_tokens, att.qo_indptr.data_ptr(), att.kv_len.data_ptr(), att.max_kv_len,
+                att.page_indptr.data_ptr(), att.page_indices.data_ptr(), w.scale, o.data_ptr(), l_.data_ptr(),
+                att.dev_status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0 and att.status() == 0
+        att.partial()
+        torch.cuda.synchronize()
+        assert torch.equal(o, att.o_parts[:w.P]) and torch.equal(l_, att.lse_parts[:w.P])
+
+
 def test_extreme_scores():
     """Capped scores far past the cap on both sides stay +-cap, and equal weights follow."""
     w = W.scored(_decode(82, 4, 1, 64, 1, 16, [40, 200], qs=2.0 ** 20), 12.0)
