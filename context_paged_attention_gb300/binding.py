@@ -244,14 +244,20 @@ def cp_kv_write(desc: PoolDesc, pool_k, pool_v, k_new, v_new, positions, qo_indp
 def _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new):
     """Types and sizes of cp_rope_kv_write's rows (by element counts first: reading five shapes costs
     as much as the launch)."""
-    dtype, hk, d, dv = desc.torch_dtype(), desc.num_kv_heads, desc.head_dim, desc.head_dim_v
-    for name, x, heads, n in (("k_new", k_new, hk, d), ("k_out", k_out, hk, d), ("v_new", v_new, hk, dv),
+    dtype, hk, d = desc.torch_dtype(), desc.num_kv_heads, desc.head_dim
+    nk, nq = T * hk * d, T * hq * d
+    if ((k_new is not None and k_new.dtype is dtype and k_new.numel() == nk and k_new.dim() == 3)
+            and (q is None or (q.dtype is dtype and q.numel() == nq and q.dim() == 3))
+            and (q_out is None or (q_out.dtype is dtype and q_out.numel() == nq and q_out.dim() == 3))
+            and (k_out is None or (k_out.dtype is dtype and k_out.numel() == nk and k_out.dim() == 3))
+            and (v_new is None or (v_new.dtype is dtype and v_new.numel() == T * hk * desc.head_dim_v
+                                   and v_new.dim() == 3))):
+        return
+    for name, x, heads, n in (("k_new", k_new, hk, d), ("k_out", k_out, hk, d), ("v_new", v_new, hk, desc.head_dim_v),
                               ("q", q, hq, d), ("q_out", q_out, hq, d)):
-        if x is None:
-            continue
-        if x.dtype is not dtype:
+        if x is not None and x.dtype is not dtype:
             raise TypeError(f"{name} must have the layer's dtype {dtype}")
-        if x.numel() != T * heads * n or x.dim() != 3:
+        if x is not None and (x.numel() != T * heads * n or x.dim() != 3):
             raise ValueError(f"{name} must be [{T}, {heads}, {n}]")
 
 
@@ -267,7 +273,7 @@ def cp_rope_kv_write(desc: PoolDesc, pool_k, pool_v, q, k_new, v_new, positions,
     if cos_sin.dim() != 2 or cos_sin.dtype is not _float32:
         raise TypeError("cos_sin must be a float32 matrix [positions, rot_dim]")
     hq = 0 if q is None else q.size(1)
-    _here(pool_k, k_new)
+    _here(pool_k)
     _check_rope_rows(desc, T, hq, q, q_out, k_new, k_out, v_new)
     st = lib.cp_rope_kv_write(ctypes.byref(desc), _ptr(pool_k), _ptr(pool_v), _ptr(q), _ptr(k_new), _ptr(v_new),
                               hq, _i32_tensor(positions, "positions"), _i32_tensor(qo_indptr, "qo_indptr"),
