@@ -1,6 +1,7 @@
 // C ABI of libcpattn (declared in include/cpattn.h): argument checks on the
 // host, then the kernel launches.  Nothing here allocates, synchronises or
 // keeps state between calls.
+#include <algorithm>
 #include <cstdint>
 
 #include "cpattn.h"
@@ -238,10 +239,11 @@ int run_partial(const cpattn_pool_desc* desc, const void* pool_k, const void* po
   a.ws_run_o = ws_part;
   a.ws_run_lse = ws_part_lse;
   if (f.fused && is_fp8(desc) && modifies(mod)) {
-    // runs of at least the stripe chunk, so that their pieces fit where the
-    // chunks' (or the partners') partials would lie: a row of L keys has
-    // ceil(L / run) of them, and there is room for P * max_chunks >= L / 2048
-    a.run = (4096 + desc->page_size - 1) / desc->page_size * desc->page_size;
+    // their pieces lie where the chunks' (or the partners') partials would: a
+    // row of L keys has ceil(L / run) of them, and there is room for P * max_chunks
+    const int room = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(desc->P) * plan.max_chunks, 1 << 20));
+    const int run = std::max(codes_run(desc->page_size, desc->num_kv_heads, num_tokens, max_kv_len), (max_kv_len + room - 1) / room);
+    a.run = (run + desc->page_size - 1) / desc->page_size * desc->page_size;
     a.max_runs = max_kv_len > 0 ? (max_kv_len + a.run - 1) / a.run : 1;
     a.ws_run_o = plan.max_chunks > 1 ? a.ws_o : ws_part;
     a.ws_run_lse = plan.max_chunks > 1 ? a.ws_lse : ws_part_lse;

@@ -153,6 +153,7 @@ struct PartialPlan {
   size_t bytes() const;
 };
 // Returns false if the shape is unsupported.
+int codes_run(int page_size, int num_kv_heads, int num_tokens, int max_kv_len);
 bool plan_partial(int mla, int fused, int fp4, int P, int interleave, int page_size, int num_kv_heads, int num_q_heads, int head_dim,
                   int num_tokens, int max_kv_len, int dtype_bytes, PartialPlan* plan);
 

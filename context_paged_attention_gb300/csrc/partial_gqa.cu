@@ -246,16 +246,18 @@ size_t PartialPlan::bytes() const {
          al(ws_part_lse_floats * 4) + al(ws_pair_ints * 4);
 }
 
-// Positions of a run of a fused call over an E2M1 pool, in whole pages: one
-// round of CTAs (four an SM) when every row has max_kv_len keys, within
-// [1024, 4096].  A CTA's start and end take some 10 us beside its neighbours'
-// work: 64 rows of 512-8192 keys took 126, 103, 93 and 86 us at runs of 512,
-// 1024, 2048 and 4096 (8 rows of 64k-128k: 458, 312, 246, 227), while few rows
-// need the split to reach every SM.
-static int fp4_fused_run(int page_size, int num_kv_heads, int num_tokens, int max_kv_len) {
+// Positions of a run of a fused decode call over a pool of codes, in whole
+// pages: one round of CTAs (three or four an SM) when every row has max_kv_len
+// keys, within [512, 4096]; rows of up to 1024 keys stay whole (a merge takes
+// 9 us: 41 rows of 929 keys 31 us, in runs of 512 40).  A CTA's start and end take some 10 us beside its
+// neighbours' work: 64 rows of 512-8192 E2M1 keys took 126, 103, 93 and 86 us
+// at runs of 512, 1024, 2048 and 4096 (8 rows of 64k-128k: 458, 312, 246, 227),
+// while few rows need the split to reach every SM.
+int codes_run(int page_size, int num_kv_heads, int num_tokens, int max_kv_len) {
   constexpr int kCtas = 4 * 152;
   const int64_t want = (static_cast<int64_t>(num_tokens) * num_kv_heads * max_kv_len + kCtas - 1) / kCtas;
-  const int run = want < 1024 ? 1024 : (want > 4096 ? 4096 : static_cast<int>(want));
+  const int least = max_kv_len > 1024 ? 512 : 1024;
+  const int run = want < least ? least : (want > 4096 ? 4096 : static_cast<int>(want));
   return (run + page_size - 1) / page_size * page_size;
 }
 
@@ -326,7 +328,7 @@ bool plan_partial(int mla, int fused, int fp4, int P, int interleave, int page_s
     plan->ws_part_lse_floats = slots * G;
     plan->ws_pair_ints = static_cast<size_t>(num_tokens) * num_kv_heads;
     if (fp4) {
-      plan->run = fp4_fused_run(page_size, num_kv_heads, num_tokens, max_kv_len);
+      plan->run = codes_run(page_size, num_kv_heads, num_tokens, max_kv_len);
       plan->max_runs = max_kv_len > 0 ? (max_kv_len + plan->run - 1) / plan->run : 1;
       if (plan->max_runs + 2 > 3000) return false;
       const size_t pieces = static_cast<size_t>(num_tokens) * num_kv_heads * plan->max_runs * G;

@@ -68,7 +68,7 @@ constexpr int kLoadWarp = 10;   // K: 10, 11, V: 12, 13
 constexpr int kUnit = 32;       // keys of a tile that one copy warp takes
 constexpr int kUnits = kTile / kUnit;
 constexpr int kThreads = 32 * (kLoadWarp + 2 * kUnits);
-constexpr int kRun = 2048;      // logical positions of a fused CTA's page run, or twice as many
+constexpr int kRun = 2048;      // logical positions of a fused CTA's page run (fewer or twice as many: see launch_t)
 constexpr int kSms = 152;
 constexpr int kMergeUnroll = 4;
 constexpr int kMergeWarps = 4;
@@ -1175,7 +1175,17 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
   Geo geo = {};
   int page_slots;
   if (a.fused) {
-    const int64_t room = static_cast<int64_t>(a.P) * a.max_chunks;  // pieces a row and head
+    // The pieces lie where the per-partner kernels keep theirs (this launch
+    // starts when theirs are done), with room for P * max_chunks a token and
+    // head; or where the decode kernel over E2M1 pools keeps its max_runs.
+    int64_t room = static_cast<int64_t>(a.P) * a.max_chunks;
+    geo.ws_o = a.max_chunks > 1 ? a.ws_o : a.o_part;
+    geo.ws_lse = a.max_chunks > 1 ? a.ws_lse : a.lse_part;
+    if (FMT == kFp4 && a.max_runs > room) {
+      room = a.max_runs;
+      geo.ws_o = a.ws_run_o;
+      geo.ws_lse = a.ws_run_lse;
+    }
     const int64_t blocks = static_cast<int64_t>(a.num_kv_heads) * ((a.num_tokens + QB - 1) / QB);
     auto runs = [&](int positions) {
       geo.run = (positions + a.page_size - 1) / a.page_size * a.page_size;
@@ -1185,7 +1195,13 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
     // merge (16 rows of 2-256 tokens on up to 8192 E2M1 keys: 243 us, runs of
     // 2048 250, of 8192 272).
     runs(kRun);
-    if (geo.max_runs * blocks > 4 * kSms) runs(2 * kRun);
+    if (geo.max_runs * blocks > 4 * kSms) {
+      runs(2 * kRun);
+    } else if (geo.max_runs * blocks < kSms) {  // few: shorter ones reach more SMs
+      const int64_t fit = (a.max_kv_len + room - 1) / room, want = (a.max_kv_len * blocks + kSms - 1) / kSms;
+      const int64_t least = fit > want ? fit : want;
+      runs(least < 256 ? 256 : (least < kRun ? static_cast<int>(least) : kRun));
+    }
     page_slots = geo.run / a.page_size + 1;
     // A CTA a run where that is about one round of CTAs.  Else all rows' pages
     // in equal parts, one a CTA, as long as a part's page ids fit: whole items
@@ -1198,14 +1214,6 @@ int launch_t(const PartialArgs& a, cudaStream_t s, cudaError_t* err) {
       geo.start = (kStart * kCost2 + a.page_size - 1) / a.page_size;
       page_slots = static_cast<int>(pages) + 1;
     }
-    // The pieces lie where the per-partner kernels keep theirs (this launch
-    // starts when theirs are done).  A row of L keys has ceil(L / run) runs,
-    // and run >= 2048, the stripe chunk (equal parts are as long as the room
-    // needs): stripes of more than one chunk have
-    // room for P * max_chunks >= L / 2048 pieces a row and head, shorter
-    // ones for P >= L / 2048.
-    geo.ws_o = a.max_chunks > 1 ? a.ws_o : a.o_part;
-    geo.ws_lse = a.max_chunks > 1 ? a.ws_lse : a.lse_part;
     if (geo.max_runs > room) return CPATTN_ERR_UNSUPPORTED_SHAPE;
     if (geo.least > 0) geo.max_runs = static_cast<int>(room);
   } else {
