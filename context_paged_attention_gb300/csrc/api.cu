@@ -127,6 +127,7 @@ size_t partial_workspace(const cpattn_pool_desc* desc, int fused, int32_t num_q_
                          int32_t max_kv_len) {
   if (check_desc(desc) != CPATTN_OK || num_q_heads < 1 || num_tokens < 0 || max_kv_len < 0) return 0;
   if (num_q_heads % desc->num_kv_heads != 0) return 0;
+  if (is_fp4(desc) && max_kv_len > (1 << 30)) return 0;  // refused by the calls
   PartialPlan plan;
   if (!plan_partial(is_mla(desc), fused, is_fp4(desc), desc->P, interleave_of(desc), desc->page_size, desc->num_kv_heads,
                     num_q_heads, desc->head_dim, num_tokens, max_kv_len, dtype_bytes(desc->dtype), &plan))

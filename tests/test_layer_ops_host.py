@@ -186,6 +186,23 @@ def test_score_mod_refusals(lib):
     assert own(m, mla=True) == -3
 
 
+def test_longest_rows(lib):
+    """Lengths that 32-bit rounding up would wrap are refused for 4-bit pools and modified scores."""
+    d, f4, m = _desc(), _desc(kv_dtype=B.DTYPE_FP4_E2M1, k_descale=0.002, v_descale=0.002), B.ScoreMod(30.0, None, None)
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        for desc, mod in ((d, m), (f4, None)):
+            assert lib.cp_paged_attn_fused_mod(ctypes.byref(desc), FAKE, FAKE, FAKE, 32, 1, 1, None, FAKE, n, FAKE, FAKE,
+                                               None, 0.1, None, None, 0, FAKE, None, mod, FAKE, 1 << 40, None, None) == -3
+            assert lib.cp_paged_attn_partial_mod(ctypes.byref(desc), FAKE, FAKE, FAKE, 32, 1, 1, None, FAKE, n, FAKE,
+                                                 FAKE, 0.1, FAKE, FAKE, 0, None, mod, FAKE, 1 << 40, None, None) == -3
+        assert lib.cp_paged_attn_fused_workspace_bytes(ctypes.byref(f4), 32, 1, n) == 0
+        assert lib.cp_paged_attn_workspace_bytes(ctypes.byref(f4), 32, 1, n) == 0
+    # multi-token rows whose pool rows pass 31 bits
+    e4 = _desc(kv_dtype=B.DTYPE_FP8_E4M3, k_descale=0.01, v_descale=0.01, num_pages=1 << 24)
+    assert lib.cp_paged_attn_fused_mod(ctypes.byref(e4), FAKE, FAKE, FAKE, 32, 1, 2, FAKE, FAKE, 100, FAKE, FAKE, None, 0.1,
+                                       None, None, 0, FAKE, None, m, FAKE, 1 << 40, None, None) == -3
+
+
 # ---------------------------------------------------------------- binding and workloads
 
 def test_binding_checks_shapes(lib):
